@@ -20,13 +20,16 @@
 
 #include "aux_kernels.hpp"
 #include "probes.hpp"
+#include "status.hpp"
 #include "decomp_kernels.hpp"
 
 using namespace fluxbin;
 
 namespace {
-
 thread_local char g_err[512] = "";
+}  // namespace
+
+namespace fluxbin {
 
 fluxbin_status fail(fluxbin_status st, const char *fmt, ...) {
   va_list ap;
@@ -45,9 +48,9 @@ fluxbin_status ok() {
   return FLUXBIN_OK;
 }
 
-bool aligned(const void *p, size_t a) { return (reinterpret_cast<uintptr_t>(p) % a) == 0; }
+}  // namespace fluxbin
 
-int64_t cdiv(int64_t a, int64_t b) { return (a + b - 1) / b; }
+namespace {
 
 constexpr int kTargetBlocks = 1024;  // about four workgroups per CU
 constexpr int kCus = 256;            // compute units of an MI355X (8 XCDs of 32)

@@ -1,0 +1,301 @@
+// logprob_kernels.hpp -- log probabilities of given tokens, the entropy and the
+// best alternatives of every row of logits, in one pass over the row.
+//
+// Mathematics.  With z_j = s x_j (s > 0 the logit scale), c = s log2(e) and m
+// the largest x_j:
+//     d_j = c (x_j - m),  S = sum 2^d_j,  D = sum 2^d_j d_j
+//     log p_j = s (x_j - m) - ln2 log2 S,  entropy = ln2 (log2 S - D / S).
+// A thread keeps (m, S, D) for the elements it has seen; two such triples are
+// joined by moving both to the larger m: with e = c (m_old - m_new) (<= 0),
+// S -> 2^e S and D -> 2^e (D + e S).  All of it is fp32.  The difference is
+// taken before the product, so that rows at the type's lowest value (a common
+// mask) stay finite; 2^d d is taken with d held at -200 or above, where 2^d is
+// 0, so that a masked logit (-inf) adds 0 and not NaN; NaN and +inf logits make
+// S NaN.
+//
+// Alternatives are ordered by key: the logit's bits as an ordered integer above
+// the complement of its index, so of equal logits the lower index is first.
+#pragma once
+
+#include "elements.hpp"
+
+namespace fluxbin {
+
+struct LogprobArgs {
+  const void *logits;
+  const int64_t *targets;                // null: no targets
+  float *logprob, *entropy, *top_logprob;  // entropy may be null
+  int64_t *top_index;
+  uint8_t *workspace;                    // splits > 1: the partial results
+  int64_t rows, ld;
+  int32_t vocab, top_k, splits, split_len;  // split_len: columns per split, a multiple of kStep
+  float scale;
+};
+
+constexpr int kLpThreads = 256;
+constexpr int kLpUnits = 4;                                // units of eight per thread and slice
+constexpr int kLpStep = kLpThreads * kUnit;                // columns of one unit of every thread
+constexpr int kLpSlice = kLpStep * kLpUnits;               // columns held in registers at a time
+constexpr int kLpMaxTop = 64;
+constexpr int kLpCap = 512;                                // candidate keys that LDS holds
+constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
+constexpr float kNegInf = -__builtin_inff();
+
+struct Stats {
+  float m, s, d;  // largest x, sum of 2^(c (x - ref(m))), that sum weighted with its exponents
+};
+
+// The reference of a largest value; 0 where there is none yet.
+__device__ __forceinline__ float ref(float m) { return m == kNegInf ? 0.0f : m; }
+
+__device__ __forceinline__ Stats join(Stats a, Stats b, float c) {
+  Stats r;
+  r.m = fmaxf(a.m, b.m);
+  const float ea = fmaxf((ref(a.m) - ref(r.m)) * c, -200.0f), eb = fmaxf((ref(b.m) - ref(r.m)) * c, -200.0f);
+  // a side without a finite logit has s = d = 0 (or NaN): its shift is of no account
+  const float ta = a.m == kNegInf ? 0.0f : ea, tb = b.m == kNegInf ? 0.0f : eb;
+  const float fa = __builtin_amdgcn_exp2f(ta), fb = __builtin_amdgcn_exp2f(tb);
+  r.s = a.s * fa + b.s * fb;
+  r.d = fmaf(ta, a.s, a.d) * fa + fmaf(tb, b.s, b.d) * fb;
+  return r;
+}
+
+// Ordered key of element `index` with value x; 0 is below every key.
+__device__ __forceinline__ uint64_t key_of(float x, int index) {
+  const int b = __builtin_bit_cast(int, x + 0.0f);  // -0 ranks as +0
+  const uint32_t o = (uint32_t)b ^ (b < 0 ? 0xffffffffu : 0x80000000u);
+  return (uint64_t)o << 32 | (uint32_t)~index;
+}
+__device__ __forceinline__ float value_of(uint64_t key) {
+  const uint32_t o = (uint32_t)(key >> 32);
+  return __builtin_bit_cast(float, (o >> 31) ? o ^ 0x80000000u : ~o);
+}
+__device__ __forceinline__ int index_of(uint64_t key) { return (int)~(uint32_t)key; }
+
+__device__ __forceinline__ Stats shuffle(Stats a, int o) {
+  return Stats{__shfl_xor(a.m, o), __shfl_xor(a.s, o), __shfl_xor(a.d, o)};
+}
+
+struct LpShared {
+  uint64_t cand[kLpCap];
+  uint64_t list[kLpMaxTop];  // the best keys so far, in order; 0 past their count
+  float tmax[kLpThreads];
+  Stats wave[kLpThreads / 64];
+  uint64_t wkey[kLpThreads / 64];
+  int count;
+  float thr;
+};
+
+// cand[0, n) -> the best top_k of them in list, in order.
+__device__ __forceinline__ void select_by_rank(LpShared &sh, int n, int top_k) {
+  if (threadIdx.x < (unsigned)kLpMaxTop) sh.list[threadIdx.x] = 0;
+  __syncthreads();
+  for (int i = threadIdx.x; i < n; i += kLpThreads) {
+    const uint64_t k = sh.cand[i];
+    int rank = 0;
+    for (int j = 0; j < n; ++j) rank += sh.cand[j] > k;
+    if (rank < top_k) sh.list[rank] = k;
+  }
+  __syncthreads();
+}
+
+__device__ __forceinline__ uint64_t block_max_key(LpShared &sh, uint64_t k) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) {
+    const uint64_t v = (uint64_t)__shfl_xor((unsigned long long)k, o);
+    k = v > k ? v : k;
+  }
+  __syncthreads();
+  if (threadIdx.x % 64 == 0) sh.wkey[threadIdx.x / 64] = k;
+  __syncthreads();
+  k = sh.wkey[0];
+#pragma unroll
+  for (int i = 1; i < kLpThreads / 64; ++i) k = sh.wkey[i] > k ? sh.wkey[i] : k;
+  return k;
+}
+
+// Writes a row's results from its joined statistics and its ordered keys.
+template <typename E>
+__device__ __forceinline__ void write_row(const LogprobArgs &a, int64_t row, Stats st, const uint64_t *list) {
+  typedef typename E::raw raw;
+  const float m = ref(st.m);
+  const float l2 = __builtin_amdgcn_logf(st.s);  // S = 0 (nothing left): -inf
+  const bool none = st.s == 0.0f;
+  auto lp = [&](float x) { return none ? kNegInf : (x - m) * a.scale - kLn2 * l2; };
+  const int t = threadIdx.x;
+  if (t == 0) {
+    if (a.targets) {
+      const int64_t target = a.targets[row];
+      float v = 0.0f;  // a negative target is no target
+      if (target >= a.vocab) v = __builtin_nanf("");
+      else if (target >= 0) v = lp(E::load(((const raw *)a.logits)[row * a.ld + target]));
+      a.logprob[row] = v;
+    }
+    if (a.entropy) a.entropy[row] = none ? 0.0f : kLn2 * (l2 - st.d / st.s);
+  }
+  if (t < a.top_k) {
+    const uint64_t k = list[t];
+    a.top_logprob[row * a.top_k + t] = k ? lp(value_of(k)) : __builtin_nanf("");
+    a.top_index[row * a.top_k + t] = k ? index_of(k) : -1;
+  }
+}
+
+// Bytes of one split's partial result: the statistics, then top_k keys.
+__host__ __device__ inline int64_t lp_part_bytes(int top_k) { return 16 + 8 * (int64_t)top_k; }
+
+// One workgroup: one split of one row.  splits == 1 writes the row's results,
+// else the split's partial result goes to the workspace.
+template <typename E>
+__global__ __launch_bounds__(kLpThreads) void logprob_rows_kernel(const LogprobArgs a) {
+  typedef typename E::raw raw;
+  __shared__ LpShared sh;
+  const int tid = threadIdx.x;
+  const int64_t row = blockIdx.x / a.splits;
+  const int split = (int)(blockIdx.x % a.splits);
+  const int begin = split * a.split_len, end = min(a.vocab, begin + a.split_len);
+  const raw *x = (const raw *)a.logits + row * a.ld;
+  const float c = a.scale * kLog2e;
+  Stats st{kNegInf, 0.0f, 0.0f};
+  float thr = kNegInf;      // candidates are above it, or equal to it while `inclusive`
+  bool inclusive = true;
+  int have = 0;             // keys in the list
+  for (int at0 = begin; at0 < end; at0 += kLpSlice) {
+    typename E::unit v[kLpUnits];
+    const int units = min(kLpUnits, (end - at0 + kLpStep - 1) / kLpStep);
+    float tm = kNegInf;
+#pragma unroll
+    for (int u = 0; u < kLpUnits; ++u) {
+      const int at = at0 + (u * kLpThreads + tid) * kUnit;
+      v[u] = load_part<E>(x, u < units ? at : end, end, kNegInf);
+    }
+#pragma unroll
+    for (int u = 0; u < kLpUnits; ++u)
+#pragma unroll
+      for (int i = 0; i < kUnit; ++i) tm = fmaxf(tm, v[u].get(i));
+    {
+      const float m = fmaxf(st.m, tm), M = ref(m);
+      Stats now{m, 0.0f, 0.0f};
+#pragma unroll
+      for (int u = 0; u < kLpUnits; ++u)
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) {
+          const float d = (v[u].get(i) - M) * c, e = __builtin_amdgcn_exp2f(d);
+          now.s += e;
+          now.d = fmaf(e, fmaxf(d, -200.0f), now.d);
+        }
+      st = join(st, now, c);
+    }
+    if (a.top_k == 0) continue;
+    // A lower bound of the slice's top_k-th value: the top_k-th largest of the threads' maxima.
+    if (inclusive && have == 0) {
+      sh.tmax[tid] = tm;
+      if (tid == 0) sh.thr = kNegInf;
+      __syncthreads();
+      int rank = 0;
+      for (int j = 0; j < kLpThreads; ++j) rank += sh.tmax[j] > tm || (sh.tmax[j] == tm && j < tid);
+      if (rank == a.top_k - 1) sh.thr = tm;
+    }
+    if (tid < have) sh.cand[tid] = sh.list[tid];
+    if (tid == 0) sh.count = have;
+    __syncthreads();
+    if (inclusive && have == 0) thr = sh.thr;
+    auto is_cand = [&](int u, int i) {
+      const float f = v[u].get(i);
+      return at0 + (u * kLpThreads + tid) * kUnit + i < end && u < units && (f > thr || (inclusive && f == thr));
+    };
+    if (tm >= thr) {
+#pragma unroll
+      for (int u = 0; u < kLpUnits; ++u)
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i)
+          if (is_cand(u, i)) {
+            const int p = atomicAdd(&sh.count, 1);
+            if (p < kLpCap) sh.cand[p] = key_of(v[u].get(i), at0 + (u * kLpThreads + tid) * kUnit + i);
+          }
+    }
+    __syncthreads();
+    const int n = sh.count;
+    if (n > have) {
+      if (n <= kLpCap) {
+        select_by_rank(sh, n, a.top_k);
+      } else {
+        // more candidates than LDS holds (long runs of equal logits): take the
+        // largest key below the last one, top_k times
+        uint64_t below = ~0ull;
+        if (tid < have) sh.cand[tid] = sh.list[tid];
+        __syncthreads();
+        const uint64_t mine = tid < have ? sh.cand[tid] : 0;
+        for (int j = 0; j < a.top_k; ++j) {
+          uint64_t best = mine < below ? mine : 0;
+#pragma unroll
+          for (int u = 0; u < kLpUnits; ++u)
+#pragma unroll
+            for (int i = 0; i < kUnit; ++i)
+              if (is_cand(u, i)) {
+                const uint64_t k = key_of(v[u].get(i), at0 + (u * kLpThreads + tid) * kUnit + i);
+                if (k < below && k > best) best = k;
+              }
+          below = block_max_key(sh, best);
+          if (tid == 0) sh.list[j] = below;
+        }
+        __syncthreads();
+      }
+      have = min(n, a.top_k);
+      if (have == a.top_k) {
+        thr = value_of(sh.list[a.top_k - 1]);
+        inclusive = false;
+      }
+    }
+    __syncthreads();
+  }
+  // join the threads' statistics
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) st = join(st, shuffle(st, o), c);
+  if (tid % 64 == 0) sh.wave[tid / 64] = st;
+  __syncthreads();
+  st = sh.wave[0];
+#pragma unroll
+  for (int i = 1; i < kLpThreads / 64; ++i) st = join(st, sh.wave[i], c);
+  if (tid >= have && tid < a.top_k) sh.list[tid] = 0;
+  __syncthreads();
+  if (a.splits == 1) {
+    write_row<E>(a, row, st, sh.list);
+  } else {
+    uint8_t *p = a.workspace + (row * a.splits + split) * lp_part_bytes(a.top_k);
+    if (tid == 0) {
+      float *f = (float *)p;
+      f[0] = st.m;
+      f[1] = st.s;
+      f[2] = st.d;
+    }
+    if (tid < a.top_k) ((uint64_t *)(p + 16))[tid] = sh.list[tid];
+  }
+}
+
+// Joins the splits of a row; splits * top_k keys, at most kLpMaxTop * kLpThreads.
+template <typename E>
+__global__ __launch_bounds__(kLpThreads) void logprob_join_kernel(const LogprobArgs a) {
+  __shared__ LpShared sh;
+  const int tid = threadIdx.x;
+  const int64_t row = blockIdx.x, pb = lp_part_bytes(a.top_k);
+  const uint8_t *base = a.workspace + row * a.splits * pb;
+  const float c = a.scale * kLog2e;
+  Stats st{kNegInf, 0.0f, 0.0f};
+  for (int i = 0; i < a.splits; ++i) {  // every thread the same, in order
+    const float *f = (const float *)(base + i * pb);
+    st = join(st, Stats{f[0], f[1], f[2]}, c);
+  }
+  // each split's list is in order: walk the heads of the lists, one list per thread
+  int head = 0;
+  const uint64_t *list = (const uint64_t *)(base + (tid < a.splits ? tid : 0) * pb + 16);
+  for (int j = 0; j < a.top_k; ++j) {
+    const uint64_t k = tid < a.splits && head < a.top_k ? list[head] : 0;
+    const uint64_t best = block_max_key(sh, k);
+    if (k == best && k) ++head;
+    if (tid == 0) sh.list[j] = best;
+  }
+  __syncthreads();
+  write_row<E>(a, row, st, sh.list);
+}
+
+}  // namespace fluxbin

@@ -25,11 +25,13 @@ ABI_VERSION = 8
 OK, ERR_INVALID_ARGUMENT, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_HIP = range(5)
 LAYOUT_ROWMAJOR, LAYOUT_TILED = 0, 1
 TABLE_F32, TABLE_F16 = 0, 1
-DT_I8, DT_F16, DT_BITS = 0, 1, 2
+DT_I8, DT_F16, DT_BITS, DT_BF16, DT_F32 = 0, 1, 2, 3, 4
 
 P = ctypes.c_void_p
 I64 = ctypes.c_int64
 I32 = ctypes.c_int32
+FLT = ctypes.c_float
+SIZE_T = ctypes.c_size_t
 
 
 class LayerDesc(ctypes.Structure):
@@ -101,6 +103,11 @@ _decl("fluxbin_decomp_col_scales", ctypes.c_int, [P, I64, I64, I32, I32, P, P, P
 _decl("fluxbin_decomp_signs", ctypes.c_int, [P, I64, I64, I32, P, P, P, P])
 _decl("fluxbin_decomp_residual_signs", ctypes.c_int, [P, I64, I64, I32, I32, P, P, P, P, P])
 _decl("fluxbin_decomp_error", ctypes.c_int, [P, I64, I64, I32, P, P, P, P, P, P, ctypes.c_size_t, P])
+_decl("fluxbin_quantize_rows", ctypes.c_int, [P, I64, I32, I64, I64, P, I64, P, P])
+_decl("fluxbin_add_rmsnorm", ctypes.c_int, [P, I64, P, I64, P, I32, I64, I64, FLT, P, I64, P, I64, P, I64, P, P])
+_decl("fluxbin_gemm_w8a8", ctypes.c_int, [P, I64, P, P, I64, P, P, I64, I64, I64, P, I64, I32, P])
+_decl("fluxbin_token_logprobs_workspace_size", ctypes.c_int, [I64, I64, I32, ctypes.POINTER(SIZE_T)])
+_decl("fluxbin_token_logprobs", ctypes.c_int, [P, I64, I32, I64, I64, FLT, P, P, P, I32, P, P, P, SIZE_T, P])
 
 SYMBOLS = [
     "fluxbin_abi_version", "fluxbin_status_string", "fluxbin_last_error", "fluxbin_tiled_words", "fluxbin_pack",
@@ -112,6 +119,8 @@ SYMBOLS = [
     "fluxbin_decomp_workspace_size",
     "fluxbin_decompose", "fluxbin_decomp_row_scales", "fluxbin_decomp_col_scales", "fluxbin_decomp_signs",
     "fluxbin_decomp_residual_signs", "fluxbin_decomp_error",
+    "fluxbin_quantize_rows", "fluxbin_add_rmsnorm", "fluxbin_gemm_w8a8", "fluxbin_token_logprobs_workspace_size",
+    "fluxbin_token_logprobs",
 ]
 
 
@@ -300,6 +309,37 @@ def fluxbin_decomp_error(w, n, k, kb, bits, r, c, col_weight, err_out, workspace
     _check(_lib.fluxbin_decomp_error(_ptr(w), n, k, kb, _ptr(bits), _ptr(r), _ptr(c), _ptr(col_weight),
                                      _ptr(err_out), _ptr(workspace), workspace_bytes, _stream(stream)),
            "fluxbin_decomp_error")
+
+
+def fluxbin_quantize_rows(x, ldx, dtype, rows, cols, q, ldq, scale, stream=None):
+    _check(_lib.fluxbin_quantize_rows(_ptr(x), ldx, dtype, rows, cols, _ptr(q), ldq, _ptr(scale), _stream(stream)),
+           "fluxbin_quantize_rows")
+
+
+def fluxbin_add_rmsnorm(x, ldx, residual, ldr, weight, dtype, rows, cols, eps, residual_out, ldro, y, ldy, q, ldq, scale,
+                        stream=None):
+    _check(_lib.fluxbin_add_rmsnorm(_ptr(x), ldx, _ptr(residual), ldr, _ptr(weight), dtype, rows, cols, eps,
+                                    _ptr(residual_out), ldro, _ptr(y), ldy, _ptr(q), ldq, _ptr(scale), _stream(stream)),
+           "fluxbin_add_rmsnorm")
+
+
+def fluxbin_gemm_w8a8(a, lda, a_scale, w, ldw, w_scale, bias, m, n, k, y, ldy, dtype, stream=None):
+    _check(_lib.fluxbin_gemm_w8a8(_ptr(a), lda, _ptr(a_scale), _ptr(w), ldw, _ptr(w_scale), _ptr(bias), m, n, k, _ptr(y),
+                                  ldy, dtype, _stream(stream)), "fluxbin_gemm_w8a8")
+
+
+def fluxbin_token_logprobs_workspace_size(rows, vocab, top_k) -> int:
+    out = SIZE_T(0)
+    _check(_lib.fluxbin_token_logprobs_workspace_size(rows, vocab, top_k, ctypes.byref(out)),
+           "fluxbin_token_logprobs_workspace_size")
+    return int(out.value)
+
+
+def fluxbin_token_logprobs(logits, ld, dtype, rows, vocab, logit_scale, targets, logprob, entropy, top_k, top_logprob,
+                           top_index, workspace, workspace_bytes, stream=None):
+    _check(_lib.fluxbin_token_logprobs(_ptr(logits), ld, dtype, rows, vocab, logit_scale, _ptr(targets), _ptr(logprob),
+                                       _ptr(entropy), top_k, _ptr(top_logprob), _ptr(top_index), _ptr(workspace),
+                                       workspace_bytes, _stream(stream)), "fluxbin_token_logprobs")
 
 
 def raw_status(name: str, *args) -> int:

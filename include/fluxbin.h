@@ -91,11 +91,14 @@ typedef enum {
   FLUXBIN_TABLE_F16 = 1  /* fp16 entries: each entry summed in fp32, rounded to fp16 (nearest even) */
 } fluxbin_table_precision;
 
-/* Element kinds for fluxbin_vcm_gather. */
+/* Element kinds: the first three for fluxbin_vcm_gather; FLUXBIN_DT_F16, _BF16
+ * and _F32 for the activations, outputs and logits of the 8-bit operators. */
 typedef enum {
-  FLUXBIN_DT_I8 = 0,  /* int8 elements, [rows][cols] */
-  FLUXBIN_DT_F16 = 1, /* fp16 elements, [rows][cols] */
-  FLUXBIN_DT_BITS = 2 /* canonical sign words [rows][ceil(cols/32)] */
+  FLUXBIN_DT_I8 = 0,   /* int8 elements, [rows][cols] */
+  FLUXBIN_DT_F16 = 1,  /* fp16 elements, [rows][cols] */
+  FLUXBIN_DT_BITS = 2, /* canonical sign words [rows][ceil(cols/32)] */
+  FLUXBIN_DT_BF16 = 3, /* bfloat16 elements (raw uint16_t bits) */
+  FLUXBIN_DT_F32 = 4   /* fp32 elements */
 } fluxbin_dtype;
 
 typedef struct fluxbin_layer *fluxbin_handle; /* opaque, immutable after create */
@@ -430,6 +433,87 @@ fluxbin_status fluxbin_decomp_residual_signs(const uint16_t *w, int64_t n, int64
 fluxbin_status fluxbin_decomp_error(const uint16_t *w, int64_t n, int64_t k, int32_t kb, const uint32_t *bits,
                                     const double *r, const double *c, const double *col_weight, double *err_out,
                                     void *workspace, size_t workspace_bytes, void *stream);
+
+/* ------------------------------------------------------------------------
+ * 8-bit operators: what stands around the binary-basis layers when the other
+ * products of a model (a prefill's projections, the output head) run in int8.
+ * A row's activations are normalised and quantised (fluxbin_add_rmsnorm,
+ * fluxbin_quantize_rows), multiplied with int8 weights (fluxbin_gemm_w8a8),
+ * and the head's logits scored (fluxbin_token_logprobs).
+ *
+ * Shared rules: dtype is FLUXBIN_DT_F16, _BF16 or _F32; a matrix is row-major
+ * with its row stride ("ld...") in elements, at least its row length; pointers
+ * need the alignment of their elements only, except the int8 operands of
+ * fluxbin_gemm_w8a8.  Zero rows launch nothing.  Arithmetic and sums are fp32
+ * (int32 for the product's sums), each output rounded once, to nearest even.
+ * The calls allocate nothing, copy nothing and do not synchronise (capturable
+ * in a HIP graph), keep nothing between calls, and give bitwise identical
+ * results on repeated calls.
+ * ------------------------------------------------------------------------ */
+
+/* Symmetric int8 of every row of x [rows][cols]:
+ *   a = max(max_j |x_j|, 2^-100),  q_j = rint(x_j * (127 / a)),
+ *   scale[row] = a / 127           (x_j ~ q_j * scale[row]).
+ * All operations are fp32 and the integers are fully determined by them.  A
+ * row that holds an infinity or a NaN gets q = 0 and scale = NaN, so that it
+ * shows in whatever is computed from it.  Weights [n][k] are quantised per
+ * output channel by the same call.  q [rows][ldq]: columns past cols are not
+ * written.  1 <= cols <= 2^30. */
+fluxbin_status fluxbin_quantize_rows(const void *x, int64_t ldx, int32_t dtype, int64_t rows, int64_t cols, int8_t *q,
+                                     int64_t ldq, float *scale, void *stream);
+
+/* Residual addition and root-mean-square norm of every row:
+ *   h = round(x + residual) in dtype (h = x when residual is NULL),
+ *   inv = 1 / sqrt(mean_j(h_j^2) + eps),
+ *   residual_out = h,  y_j = h_j * inv * weight_j,
+ *   t_j = h_j * weight_j,  a = max(max_j |t_j|, 2^-100),
+ *   q_j = rint(t_j * (127 / a)),  scale[row] = (a / 127) * inv
+ *                                  (y_j ~ q_j * scale[row]).
+ * y, q (with scale) and residual_out may each be NULL, y and q not both;
+ * residual_out needs residual and may be x or residual itself with the same
+ * stride.  weight: [cols] in dtype.  The factor inv is common to the row, so
+ * the integers do not depend on it.  A row with an infinite or NaN h (or t)
+ * gets q = 0 and scale = NaN; where the sum of h^2 is not finite in fp32
+ * (fp32 and bf16 rows with values beyond about 1e19) inv is NaN.  eps is
+ * finite and >= 0; with eps = 0 a row of zeros has y = NaN and scale = inf. */
+fluxbin_status fluxbin_add_rmsnorm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight,
+                                   int32_t dtype, int64_t rows, int64_t cols, float eps, void *residual_out, int64_t ldro,
+                                   void *y, int64_t ldy, int8_t *q, int64_t ldq, float *scale, void *stream);
+
+/* y[i][j] = (sum_l a[i][l] * w[j][l]) * a_scale[i] * w_scale[j] + bias[j]:
+ * a int8 [m][lda], w int8 [n][ldw], a_scale fp32 [m], w_scale fp32 [n], bias
+ * fp32 [n] or NULL, y [m][ldy] in dtype.  The sum is exact (int32); it is
+ * rounded to fp32, scaled and shifted in that order and rounded once to dtype.
+ * a and w must be 16-byte aligned and lda, ldw multiples of 16 that are at
+ * least k rounded up to 16; the bytes of a row between k and that multiple are
+ * read but do not count, whatever they hold.  1 <= k <= 131071 (the sums of
+ * any int8 values stay in int32), m and n at most 2^28. */
+fluxbin_status fluxbin_gemm_w8a8(const int8_t *a, int64_t lda, const float *a_scale, const int8_t *w, int64_t ldw,
+                                 const float *w_scale, const float *bias, int64_t m, int64_t n, int64_t k, void *y,
+                                 int64_t ldy, int32_t dtype, void *stream);
+
+/* Scores of every row of logits x [rows][vocab], z = logit_scale * x (the scale
+ * is an inverse temperature, > 0):
+ *   logprob[row] = z[targets[row]] - log(sum_j exp(z_j)); 0 for a negative
+ *     target (a position without one), NaN for a target >= vocab;
+ *   entropy[row] = -sum_j p_j log p_j in nats, p = softmax(z);
+ *   top_index[row][0..top_k), top_logprob[row][0..top_k): the top_k largest
+ *     logits in descending order, of equal ones the lowest index first, and
+ *     their log probabilities.
+ * targets (int64 [rows]) and logprob are both given or both NULL; entropy may
+ * be NULL; 0 <= top_k <= min(vocab, 64).  A masked logit (-inf) has
+ * probability 0 and log probability -inf and adds 0 to the entropy.  A row
+ * that is masked throughout has log probabilities -inf and entropy 0.  A row
+ * with a NaN or +inf logit has NaN log probabilities and entropy; a NaN is
+ * never an alternative, and slots left over hold index -1.  workspace: at
+ * least fluxbin_token_logprobs_workspace_size() bytes (never above 4 MiB),
+ * 16-byte aligned, free for other use once the call's work has finished; NULL
+ * where that size is 0.  rows <= 2^22, vocab <= 2^28. */
+fluxbin_status fluxbin_token_logprobs_workspace_size(int64_t rows, int64_t vocab, int32_t top_k, size_t *bytes);
+fluxbin_status fluxbin_token_logprobs(const void *logits, int64_t ld, int32_t dtype, int64_t rows, int64_t vocab,
+                                      float logit_scale, const int64_t *targets, float *logprob, float *entropy,
+                                      int32_t top_k, float *top_logprob, int64_t *top_index, void *workspace,
+                                      size_t workspace_bytes, void *stream);
 
 #ifdef __cplusplus
 }
