@@ -8,13 +8,23 @@ using namespace fluxbin;
 namespace {
 
 constexpr int64_t kMaxK = 131071;            // 131071 * 128 * 128 < 2^31
-constexpr int64_t kMaxMN = (int64_t)1 << 28;
+constexpr int64_t kMaxMN = (int64_t)1 << 27;
+constexpr int64_t kTileStride = (int64_t)1 << 23;  // 256 strides stay below 2^31 (32-bit offsets)
+
+template <typename E, int BN, int BM, int WN, int WM>
+void launch_tile(const GemmArgs &g, hipStream_t st) {
+  hipLaunchKernelGGL((gemm_w8a8_tile_kernel<E, BN, BM, WN, WM>), dim3((unsigned)(cdiv(g.n, BN) * cdiv(g.m, BM))),
+                     dim3(64 * WN * WM), 0, st, g);
+}
 
 template <typename E>
 void launch(const GemmArgs &g, hipStream_t st) {
   const unsigned nb = (unsigned)cdiv(g.n, 16);
   if (g.m <= 16) hipLaunchKernelGGL((gemm_w8a8_rows_kernel<E, 1, 4>), dim3(nb, 1), dim3(256), 0, st, g);
-  else hipLaunchKernelGGL((gemm_w8a8_rows_kernel<E, 4, 4>), dim3(nb, (unsigned)cdiv(g.m, 64)), dim3(256), 0, st, g);
+  else if (g.m <= 64 || g.lda > kTileStride || g.ldw > kTileStride)
+    hipLaunchKernelGGL((gemm_w8a8_rows_kernel<E, 4, 4>), dim3(nb, (unsigned)cdiv(g.m, 64)), dim3(256), 0, st, g);
+  else if (g.m <= 1024) launch_tile<E, 64, 64, 2, 2>(g, st);
+  else launch_tile<E, 256, 256, 2, 4>(g, st);
 }
 
 }  // namespace
@@ -28,7 +38,7 @@ extern "C" fluxbin_status fluxbin_gemm_w8a8(const int8_t *a, int64_t lda, const 
   if (k < 1) return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "k = %lld (must be >= 1)", (long long)k);
   if (k > kMaxK) return fail(FLUXBIN_ERR_UNSUPPORTED, "k = %lld above %lld: the sums could leave int32", (long long)k,
                              (long long)kMaxK);
-  if (m > kMaxMN || n > kMaxMN) return fail(FLUXBIN_ERR_UNSUPPORTED, "m or n above 2^28");
+  if (m > kMaxMN || n > kMaxMN) return fail(FLUXBIN_ERR_UNSUPPORTED, "m or n above 2^27");
   if (m == 0 || n == 0) return ok();
   if (!a || !a_scale || !w || !w_scale || !y) return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "NULL pointer");
   if (!aligned(a, 16) || !aligned(w, 16)) return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "a and w must be 16-byte aligned");

@@ -487,7 +487,7 @@ fluxbin_status fluxbin_add_rmsnorm(const void *x, int64_t ldx, const void *resid
  * a and w must be 16-byte aligned and lda, ldw multiples of 16 that are at
  * least k rounded up to 16; the bytes of a row between k and that multiple are
  * read but do not count, whatever they hold.  1 <= k <= 131071 (the sums of
- * any int8 values stay in int32), m and n at most 2^28. */
+ * any int8 values stay in int32), m and n at most 2^27. */
 fluxbin_status fluxbin_gemm_w8a8(const int8_t *a, int64_t lda, const float *a_scale, const int8_t *w, int64_t ldw,
                                  const float *w_scale, const float *bias, int64_t m, int64_t n, int64_t k, void *y,
                                  int64_t ldy, int32_t dtype, void *stream);

@@ -69,7 +69,7 @@ def gemm_args(**kw):
 
 @pytest.mark.parametrize("kw,status", [
     (dict(dtype=0), 2), (dict(m=-1), 1), (dict(n=-1), 1), (dict(k=0), 1), (dict(k=131072, lda=131072, ldw=131072), 2),
-    (dict(m=(1 << 28) + 1), 2), (dict(n=(1 << 28) + 1), 2), (dict(a=None), 1), (dict(w=None), 1), (dict(a_scale=None), 1),
+    (dict(m=(1 << 27) + 1), 2), (dict(n=(1 << 27) + 1), 2), (dict(a=None), 1), (dict(w=None), 1), (dict(a_scale=None), 1),
     (dict(w_scale=None), 1), (dict(y=None), 1), (dict(a=A + 8), 1), (dict(w=A + 8), 1), (dict(lda=72), 1), (dict(ldw=72), 1),
     (dict(lda=48), 1), (dict(k=65, lda=80), 1), (dict(ldy=7), 1), (dict(y=A + 1), 1), (dict(dtype=4, y=A + 2), 1),
     (dict(bias=A + 2), 1), (dict(a_scale=A + 1), 1), (dict(w_scale=A + 1), 1),
