@@ -11,9 +11,9 @@ constexpr int64_t kMaxK = 131071;            // 131071 * 128 * 128 < 2^31
 constexpr int64_t kMaxMN = (int64_t)1 << 27;
 constexpr int64_t kTileStride = (int64_t)1 << 23;  // 256 strides stay below 2^31 (32-bit offsets)
 
-template <typename E, int BN, int BM, int WN, int WM>
+template <typename E, int BN, int BM, int WN, int WM, int S, int G>
 void launch_tile(const GemmArgs &g, hipStream_t st) {
-  hipLaunchKernelGGL((gemm_w8a8_tile_kernel<E, BN, BM, WN, WM>), dim3((unsigned)(cdiv(g.n, BN) * cdiv(g.m, BM))),
+  hipLaunchKernelGGL((gemm_w8a8_tile_kernel<E, BN, BM, WN, WM, S, G>), dim3((unsigned)(cdiv(g.n, BN) * cdiv(g.m, BM))),
                      dim3(64 * WN * WM), 0, st, g);
 }
 
@@ -23,8 +23,8 @@ void launch(const GemmArgs &g, hipStream_t st) {
   if (g.m <= 16) hipLaunchKernelGGL((gemm_w8a8_rows_kernel<E, 1, 4>), dim3(nb, 1), dim3(256), 0, st, g);
   else if (g.m <= 64 || g.lda > kTileStride || g.ldw > kTileStride)
     hipLaunchKernelGGL((gemm_w8a8_rows_kernel<E, 4, 4>), dim3(nb, (unsigned)cdiv(g.m, 64)), dim3(256), 0, st, g);
-  else if (g.m <= 1024) launch_tile<E, 64, 64, 2, 2>(g, st);
-  else launch_tile<E, 256, 256, 2, 4>(g, st);
+  else if (g.m <= 1024) launch_tile<E, 64, 64, 2, 2, 4, 4>(g, st);
+  else launch_tile<E, 256, 256, 2, 4, 2, 1>(g, st);
 }
 
 }  // namespace

@@ -75,8 +75,7 @@ __device__ __forceinline__ i32x4 mask_tail(i32x4 v, int at, int k) {
 // One workgroup: 16 output channels x 16 MT tokens; its KW waves take blocks of
 // 256 columns in turn and add their sums in LDS.  Both operands go from global
 // memory into the registers of v_mfma_i32_16x16x64_i8: lane l holds row l % 16
-// and, of each block, the 64 bytes from (l / 16) * 64 on (any order of k serves
-// as long as both operands share it).
+// and, of each 64 columns, the 16 bytes from (l / 16) * 16 on.
 template <typename E, int MT, int KW>
 __global__ __launch_bounds__(64 * KW) void gemm_w8a8_rows_kernel(const GemmArgs g) {
   constexpr int KB = 256;
@@ -96,7 +95,7 @@ __global__ __launch_bounds__(64 * KW) void gemm_w8a8_rows_kernel(const GemmArgs 
     i32x4 wv[4], av[MT][4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int at = kb + c * 64 + j * 16, from = min(at, last);
+      const int at = kb + j * 64 + c * 16, from = min(at, last);
       wv[j] = *reinterpret_cast<const i32x4 *>(wr + from);
 #pragma unroll
       for (int t = 0; t < MT; ++t) av[t][j] = *reinterpret_cast<const i32x4 *>(ar[t] + from);
@@ -105,7 +104,7 @@ __global__ __launch_bounds__(64 * KW) void gemm_w8a8_rows_kernel(const GemmArgs 
 #pragma unroll
       for (int j = 0; j < 4; ++j)
 #pragma unroll
-        for (int t = 0; t < MT; ++t) av[t][j] = mask_tail(av[t][j], kb + c * 64 + j * 16, g.k);
+        for (int t = 0; t < MT; ++t) av[t][j] = mask_tail(av[t][j], kb + j * 64 + c * 16, g.k);
     }
 #pragma unroll
     for (int j = 0; j < 4; ++j)
@@ -141,40 +140,54 @@ __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t base, uint32_
   __builtin_amdgcn_raw_ptr_buffer_load_lds(base, (FB_LDS void *)dst, 16, voff, soff, 0, 0);
 }
 
+// Waits until at most `vm` of the wave's vector-memory operations and none of
+// its LDS operations are outstanding, then for the workgroup.
+template <int VM>
+__device__ __forceinline__ void wait_and_meet() {
+  static_assert(VM < 64, "vmcnt has six bits");
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_s_waitcnt((VM & 15) | 7 << 4 | (VM >> 4) << 14);  // lgkmcnt 0, expcnt any
+  __builtin_amdgcn_s_barrier();
+  asm volatile("" ::: "memory");
+  __builtin_amdgcn_sched_barrier(0);
+}
+
 // LDS-tiled product: BN channels x BM tokens per workgroup, WN x WM waves, 128
-// bytes of k per stage, two stages in LDS.  A stage keeps each row's eight
-// 16-byte pieces at positions exchanged by the row's number (piece p of row r
-// at p ^ (r % 8)), so that the lanes of a fragment read, which take one piece
-// of consecutive rows, spread over the banks; the exchange is made in the
-// global addresses, since a direct load writes LDS in lane order.
-template <typename E, int BN, int BM, int WN, int WM>
+// bytes of k per stage, S stages in LDS of which S - 1 are loaded ahead.  A
+// stage keeps each row's eight 16-byte pieces at positions exchanged by the
+// row's number (piece p of row r at p ^ (r / 2 % 8)), so that the 16 lanes of a
+// fragment read that the LDS serves at once, which take one piece of
+// consecutive rows, fall into all 64 banks; the exchange is made in the global
+// addresses, since a direct load writes LDS in lane order.
+//
+// Fragments are read one step ahead of the products; a step is G of a stage's
+// four 32-byte blocks of k.  Large wave tiles take G = 1 (a step's products
+// outlast the reads of the next), small ones the whole stage (G = 4), so that
+// a stage waits for LDS once and not four times.
+template <typename E, int BN, int BM, int WN, int WM, int S, int G>
 __global__ __launch_bounds__(64 * WN * WM) void gemm_w8a8_tile_kernel(const GemmArgs g) {
-  constexpr int KB = 128, W = WN * WM, STEPS = KB / 32;
+  constexpr int KB = 128, W = WN * WM, STEPS = KB / 32 / G, STAGE = (BN + BM) * KB;
   constexpr int NT = BN / WN / 32, MT = BM / WM / 32;  // 32 x 32 tiles of a wave
   constexpr int LW = BN / 8 / W, LA = BM / 8 / W;      // direct loads (8 rows each) of a wave per stage
   static_assert(BN % (8 * W) == 0 && BM % (8 * W) == 0, "rows divide over the waves");
-  // two arrays, so that the compiler sees that reads of one stage do not wait
-  // for the direct loads of the other
-  __shared__ __align__(1024) int8_t buf0[(BN + BM) * KB];
-  __shared__ __align__(1024) int8_t buf1[(BN + BM) * KB];
+  __shared__ __align__(1024) int8_t lds[S * STAGE];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   // Workgroups go to the 8 XCDs in turn: each XCD takes a contiguous eighth of
   // the tiles, in panels of kPanel token blocks, so that the workgroups that
   // share an L2 share operands.
   constexpr int kPanel = 4;
   const int nb = (g.n + BN - 1) / BN, mb = (g.m + BM - 1) / BM;
-  int t0;
+  int tile;
   {
     const int total = nb * mb, xcd = blockIdx.x % 8, pos = blockIdx.x / 8;
     const int per = total / 8, rest = total % 8;
-    t0 = xcd * per + min(xcd, rest) + pos;
+    tile = xcd * per + min(xcd, rest) + pos;
   }
-  const int panel = t0 / (kPanel * nb), in = t0 % (kPanel * nb), wide = min(kPanel, mb - panel * kPanel);
+  const int panel = tile / (kPanel * nb), in = tile % (kPanel * nb), wide = min(kPanel, mb - panel * kPanel);
   const int n0 = in / wide * BN, m0 = (panel * kPanel + in % wide) * BM;
   const int last = (g.k - 1) / 16 * 16;
-  const int piece = ((lane % 8) ^ (lane / 8)) * 16;
-  // a uniform base and a 32-bit offset per lane (the host keeps 256 strides
-  // below 2^31); rows past the matrix repeat its last one
+  // The loads' uniform bases and 32-bit offsets per lane (the host keeps 256
+  // strides below 2^31); rows past the matrix repeat its last one.
   const __amdgpu_buffer_rsrc_t from_w = buffer_of(g.w + n0 * g.ldw), from_a = buffer_of(g.a + m0 * g.lda);
   uint32_t off_w[LW], off_a[LA];
 #pragma unroll
@@ -183,12 +196,19 @@ __global__ __launch_bounds__(64 * WN * WM) void gemm_w8a8_tile_kernel(const Gemm
   for (int i = 0; i < LA; ++i) off_a[i] = (uint32_t)min((wave * LA + i) * 8 + lane / 8, g.m - 1 - m0) * (uint32_t)g.lda;
   auto fetch = [&](int stage, int8_t *buf) {
     const int k0 = stage * KB;
-    const uint32_t at = min(piece, last - k0);
+    // the lane's piece in blocks of 8 rows of even and of odd number
+    uint32_t at[2];
+#pragma unroll
+    for (int odd = 0; odd < 2; ++odd) at[odd] = min(((lane % 8) ^ (4 * odd + lane / 16)) * 16, last - k0);
     FB_LDS int8_t *dst = (FB_LDS int8_t *)buf;
 #pragma unroll
-    for (int i = 0; i < LW; ++i) load_to_lds(from_w, off_w[i] + at, k0, dst + (wave * LW + i) * 1024);
+    for (int i = 0; i < LW; ++i) load_to_lds(from_w, off_w[i] + at[(wave * LW + i) % 2], k0, dst + (wave * LW + i) * 1024);
 #pragma unroll
-    for (int i = 0; i < LA; ++i) load_to_lds(from_a, off_a[i] + at, k0, dst + BN * KB + (wave * LA + i) * 1024);
+    for (int i = 0; i < LA; ++i)
+      load_to_lds(from_a, off_a[i] + at[(wave * LA + i) % 2], k0, dst + BN * KB + (wave * LA + i) * 1024);
+  };
+  auto piece_at = [](int8_t *buf, int row, int p) {
+    return reinterpret_cast<i32x4 *>(buf + row * KB + ((p ^ (row / 2 % 8)) * 16));
   };
   const int stages = (g.k + KB - 1) / KB;
   // Where k ends inside a stage, the tokens' pieces behind it are cleared (what
@@ -196,9 +216,8 @@ __global__ __launch_bounds__(64 * WN * WM) void gemm_w8a8_tile_kernel(const Gemm
   auto clear_tail = [&](int8_t *buf) {
     const int left = g.k - (stages - 1) * KB;
     for (int i = threadIdx.x; i < BM * 8; i += 64 * W) {
-      const int row = BN + i / 8, p = i % 8;
-      i32x4 *at = reinterpret_cast<i32x4 *>(buf + row * KB + ((p ^ (row % 8)) * 16));
-      if (p * 16 + 16 > left) *at = mask_tail(*at, p * 16, left);
+      i32x4 *at = piece_at(buf, BN + i / 8, i % 8);
+      if (i % 8 * 16 + 16 > left) *at = mask_tail(*at, i % 8 * 16, left);
     }
   };
   const int wn = wave / WM, wm = wave % WM;
@@ -208,73 +227,94 @@ __global__ __launch_bounds__(64 * WN * WM) void gemm_w8a8_tile_kernel(const Gemm
   for (int i = 0; i < NT; ++i)
 #pragma unroll
     for (int j = 0; j < MT; ++j) acc[i][j] = i32x16{};
-  i32x4 wv[2][NT], av[2][MT];
-  auto load_step = [&](const int8_t *buf, int s, int set) {
-    const int p = 2 * s + half;
+  i32x4 wv[2][G][NT], av[2][G][MT];
+  auto load_step = [&](int8_t *buf, int s, int set) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i) {
-      const int row = (wn * NT + i) * 32 + r;
-      wv[set][i] = *reinterpret_cast<const i32x4 *>(buf + row * KB + ((p ^ (row % 8)) * 16));
-    }
+    for (int b = 0; b < G; ++b) {
+      const int p = 2 * (s * G + b) + half;
 #pragma unroll
-    for (int j = 0; j < MT; ++j) {
-      const int row = BN + (wm * MT + j) * 32 + r;
-      av[set][j] = *reinterpret_cast<const i32x4 *>(buf + row * KB + ((p ^ (row % 8)) * 16));
+      for (int i = 0; i < NT; ++i) wv[set][b][i] = *piece_at(buf, (wn * NT + i) * 32 + r, p);
+#pragma unroll
+      for (int j = 0; j < MT; ++j) av[set][b][j] = *piece_at(buf, BN + (wm * MT + j) * 32 + r, p);
     }
   };
   auto multiply = [&](int set) {
 #pragma unroll
-    for (int i = 0; i < NT; ++i)
+    for (int b = 0; b < G; ++b)
 #pragma unroll
-      for (int j = 0; j < MT; ++j) acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[set][i], av[set][j], acc[i][j], 0, 0, 0);
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j)
+          acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[set][b][i], av[set][b][j], acc[i][j], 0, 0, 0);
   };
-  // One stage: its fragments are read one step ahead of the products, all reads
-  // of a step before its products, so that they land while the products run.
-  // The barrier that ends the stage's reads and the next stage's loads stands
-  // before the last step's products, which cover the first reads after it.
-  auto run_stage = [&](int t, int8_t *cur, int8_t *nxt, auto more) {
-    if (more()) fetch(t + 1, nxt);
-    __builtin_amdgcn_sched_barrier(0);
+  // Stage t + 1 has landed for every wave, and every wave has read stage t.
+  auto next_landed = [&](int t) {
+    if (t + S <= stages) wait_and_meet<(S - 2) * (LW + LA)>();  // the loads of S - 2 later stages may be in flight
+    else wait_and_meet<0>();
+    if (t + 2 == stages && g.k % KB) {
+      clear_tail(lds + (t + 1) % S * STAGE);
+      wait_and_meet<0>();
+    }
+  };
+  // One stage that another follows; its first step's fragments are in set
+  // `first`.  All reads of a step stand before the products of the step before,
+  // and the barrier that ends the stage's reads before the last step's
+  // products, which cover the first reads and the loads behind it.
+  auto run_stage = [&](int t, int8_t *cur, int8_t *nxt, int first) {
 #pragma unroll
     for (int s = 0; s + 1 < STEPS; ++s) {
-      load_step(cur, s + 1, (s + 1) % 2);
-      multiply(s % 2);
-      __builtin_amdgcn_sched_group_barrier(0x100, NT + MT, 0);  // LDS reads
-      __builtin_amdgcn_sched_group_barrier(0x008, NT * MT, 0);  // products
+      load_step(cur, s + 1, (first + s + 1) % 2);
+      multiply((first + s) % 2);
+      __builtin_amdgcn_sched_group_barrier(0x100, G * (NT + MT), 0);  // LDS reads
+      __builtin_amdgcn_sched_group_barrier(0x008, G * NT * MT, 0);    // products
       __builtin_amdgcn_sched_barrier(0);
     }
-    if (more()) {
-      __syncthreads();
-      if (t + 2 == stages && g.k % KB) {
-        clear_tail(nxt);
-        __syncthreads();
-      }
-      load_step(nxt, 0, 0);
-      __builtin_amdgcn_sched_barrier(0);
-    }
-    multiply((STEPS - 1) % 2);
+    next_landed(t);
+    load_step(nxt, 0, (first + STEPS) % 2);
+    if (t + S < stages) fetch(t + S, cur);
+    __builtin_amdgcn_sched_barrier(0);
+    multiply((first + STEPS - 1) % 2);
     __builtin_amdgcn_sched_barrier(0);
   };
-  const auto yes = [] { return true; };
-  const auto no = [] { return false; };
-  fetch(0, buf0);
-  __syncthreads();
+#pragma unroll
+  for (int i = 0; i < S; ++i)
+    if (i < stages) fetch(i, lds + i * STAGE);
+  if (stages >= S) wait_and_meet<(S - 1) * (LW + LA)>();
+  else wait_and_meet<0>();
   if (stages == 1 && g.k % KB) {
-    clear_tail(buf0);
-    __syncthreads();
+    clear_tail(lds);
+    wait_and_meet<0>();
   }
-  load_step(buf0, 0, 0);
-  int t = 0;
-  for (; t + 2 < stages; t += 2) {
-    run_stage(t, buf0, buf1, yes);
-    run_stage(t + 1, buf1, buf0, yes);
+  load_step(lds, 0, 0);
+  int slot = 0, t = 0;
+  auto go = [&](int first) {
+    const int next = slot + 1 == S ? 0 : slot + 1;
+    run_stage(t++, lds + slot * STAGE, lds + next * STAGE, first);
+    slot = next;
+  };
+  if (STEPS % 2) {  // a stage of one step: the sets take turns by stage
+    while (t + 2 < stages) {
+      go(0);
+      go(1);
+    }
+    if (t + 1 < stages) {
+      go(0);
+#pragma unroll
+      for (int b = 0; b < G; ++b) {
+#pragma unroll
+        for (int i = 0; i < NT; ++i) wv[0][b][i] = wv[1][b][i];
+#pragma unroll
+        for (int j = 0; j < MT; ++j) av[0][b][j] = av[1][b][j];
+      }
+    }
+  } else {
+    while (t + 1 < stages) go(0);
   }
-  int8_t *final = buf0;
-  if (t + 1 < stages) {
-    run_stage(t, buf0, buf1, yes);
-    final = buf1;
+#pragma unroll
+  for (int s = 0; s < STEPS; ++s) {
+    if (s + 1 < STEPS) load_step(lds + slot * STAGE, s + 1, (s + 1) % 2);
+    multiply(s % 2);
   }
-  run_stage(stages - 1, final, nullptr, no);
   // The epilogue's addresses are not to be computed before the loop and held in
   // registers through it.
   int ne = n0 + wn * NT * 32 + 4 * half, me = m0 + wm * MT * 32 + r;
