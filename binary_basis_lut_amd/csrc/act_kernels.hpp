@@ -63,7 +63,8 @@ __device__ __forceinline__ void wave_reduce(float &ss, uint32_t &ab) {
   }
 }
 
-__device__ __forceinline__ void store_q(int8_t *row, int64_t at, int64_t n, const float (&t)[kUnit], const RowScale &r) {
+template <typename I>
+__device__ __forceinline__ void store_q(int8_t *row, I at, I n, const float (&t)[kUnit], const RowScale &r) {
   uint32_t b[kUnit];
 #pragma unroll
   for (int i = 0; i < kUnit; ++i) b[i] = r.finite ? (uint32_t)(int)rintf(t[i] * r.mul) & 0xffu : 0u;
@@ -99,55 +100,72 @@ __device__ __forceinline__ void take_unit(typename E::unit &h, const typename E:
 }
 
 // Writes a unit's y and q.
-template <typename E, bool NORM>
-__device__ __forceinline__ void give_unit(const ActArgs &a, int64_t row, int64_t at, const typename E::unit &h,
+template <typename E, bool NORM, typename I>
+__device__ __forceinline__ void give_unit(const ActArgs &a, int64_t row, I at, const typename E::unit &h,
                                           const typename E::unit &w, const RowScale &rs) {
   typedef typename E::raw raw;
   float t[kUnit];
 #pragma unroll
   for (int i = 0; i < kUnit; ++i) t[i] = NORM ? h.get(i) * w.get(i) : h.get(i);
-  if (a.q) store_q(a.q + row * a.ldq, at, a.cols, t, rs);
+  if (a.q) store_q<I>(a.q + row * a.ldq, at, (I)a.cols, t, rs);
   if (NORM && a.y) {
     typename E::unit y;
     float f[kUnit];
 #pragma unroll
     for (int i = 0; i < kUnit; ++i) f[i] = h.get(i) * rs.inv * w.get(i);
     y.set(f);
-    store_part<E>((raw *)a.y + row * a.ldy, at, a.cols, y);
+    store_part<E, I>((raw *)a.y + row * a.ldy, at, (I)a.cols, y);
   }
 }
 
+// Memory-bound: a row is read once and its results written once, and what
+// matters is how many bytes of how many rows a CU has in flight, so the row's
+// units stay in registers as they are stored and the instances are chosen for
+// 64 registers or fewer where that is possible.  MI355X: 8192 x 8192 fp16 with a
+// residual (470 MB) 84 us = 5.6 TB/s, 4096 x 4096 24.4 us; fp16 to int8 alone,
+// 8192 x 28672 (705 MB) 145 us = 4.9 TB/s, 30000 x 4000 66 us; one row of 4096
+// 3.5 us against 1.6 us of an empty launch.
+//
 // TPR threads per row (64: one wave, several rows to a workgroup), U units of
-// eight elements per thread; the row has at most TPR * U * 8 columns.
+// eight elements per thread; the row has at least 8 and at most TPR * U * 8
+// columns.
 template <typename E, bool NORM, int TPR, int U>
-__global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void act_rows_kernel(const ActArgs a) {
+__global__ __launch_bounds__(TPR < 256 ? 256 : TPR)
+__attribute__((amdgpu_waves_per_eu(TPR == 1024 && U <= 2 && sizeof(typename E::raw) == 2 ? 8 : 1))) void act_rows_kernel(const ActArgs a) {
   typedef typename E::raw raw;
   constexpr int TPB = TPR < 256 ? 256 : TPR, RPB = TPB / TPR, WPR = TPR / 64;
   __shared__ float s_ss[TPB / 64];
   __shared__ uint32_t s_ab[TPB / 64];
-  const int lane = threadIdx.x % TPR, slot = threadIdx.x / TPR;
+  const int lane = threadIdx.x % TPR, slot = RPB == 1 ? 0 : threadIdx.x / TPR;
   const bool add = NORM && a.residual;
   for (int64_t r0 = (int64_t)blockIdx.x * RPB; r0 < a.rows; r0 += (int64_t)gridDim.x * RPB) {
     const int64_t row = r0 + slot;
     const bool live = row < a.rows;
-    const int64_t n = live ? a.cols : 0;
+    const int n = live ? (int)a.cols : 0;
     const raw *x = (const raw *)a.x + row * a.ldx, *res = (const raw *)a.residual + row * a.ldr;
     const raw *wt = (const raw *)a.weight;
     typename E::unit h[U], rv[U], wv[U];
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t at = (int64_t)(u * TPR + lane) * kUnit;
-      h[u] = load_part<E>(x, at, n, 0.0f);
-      if (add) rv[u] = load_part<E>(res, at, n, 0.0f);
-      if (NORM) wv[u] = load_part<E>(wt, at, n, 0.0f);
+      const int at = (u * TPR + lane) * kUnit;
+      h[u] = load_part<E, false, int>(x, at, n, 0.0f);
+      if (add) rv[u] = load_part<E, false, int>(res, at, n, 0.0f);
+      if (NORM) wv[u] = load_part<E, false, int>(wt, at, n, 0.0f);
     }
     float ss = 0.0f;
     uint32_t ab = 0;
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t at = (int64_t)(u * TPR + lane) * kUnit;
+      const int at = (u * TPR + lane) * kUnit;
+      settle_part<E, false, int>(h[u], at, n, 0.0f);
+      if (add) settle_part<E, false, int>(rv[u], at, n, 0.0f);
+      if (NORM) settle_part<E, false, int>(wv[u], at, n, 0.0f);
       take_unit<E, NORM>(h[u], rv[u], wv[u], add, ss, ab);
-      if (NORM && a.residual_out) store_part<E>((raw *)a.residual_out + row * a.ldro, at, n, h[u]);
+      if (NORM && a.residual_out) store_part<E, int>((raw *)a.residual_out + row * a.ldro, at, n, h[u]);
+      if (NORM) {
+        h[u].hold();
+        wv[u].hold();
+      }
     }
     wave_reduce(ss, ab);
     if (WPR > 1) {
@@ -168,15 +186,15 @@ __global__ __launch_bounds__(TPR < 256 ? 256 : TPR) void act_rows_kernel(const A
     const RowScale rs = row_scale(ss, ab, NORM, a.inv_cols, a.eps);
 #pragma unroll
     for (int u = 0; u < U; ++u) {
-      const int64_t at = (int64_t)(u * TPR + lane) * kUnit;
-      if (at < n) give_unit<E, NORM>(a, row, at, h[u], wv[u], rs);
+      const int at = (u * TPR + lane) * kUnit;
+      if (at < n) give_unit<E, NORM, int>(a, row, at, h[u], wv[u], rs);
     }
     if (live && a.q && lane == 0) a.scale[row] = rs.scale;
   }
 }
 
-// Rows beyond the registers of a workgroup: two passes over the row, the
-// second one from the caches.
+// Rows beyond the registers of a workgroup, and rows shorter than a unit: two
+// passes over the row, the second one from the caches.
 template <typename E, bool NORM>
 __global__ __launch_bounds__(1024) void act_long_rows_kernel(const ActArgs a) {
   typedef typename E::raw raw;
@@ -191,9 +209,9 @@ __global__ __launch_bounds__(1024) void act_long_rows_kernel(const ActArgs a) {
     float ss = 0.0f;
     uint32_t ab = 0;
     for (int64_t at = (int64_t)threadIdx.x * kUnit; at < n; at += 1024 * kUnit) {
-      typename E::unit h = load_part<E>(x, at, n, 0.0f), rv, wv;
-      if (add) rv = load_part<E>(res, at, n, 0.0f);
-      if (NORM) wv = load_part<E>(wt, at, n, 0.0f);
+      typename E::unit h = load_part<E, true, int64_t>(x, at, n, 0.0f), rv, wv;
+      if (add) rv = load_part<E, true, int64_t>(res, at, n, 0.0f);
+      if (NORM) wv = load_part<E, true, int64_t>(wt, at, n, 0.0f);
       take_unit<E, NORM>(h, rv, wv, add, ss, ab);
     }
     wave_reduce(ss, ab);
@@ -214,14 +232,14 @@ __global__ __launch_bounds__(1024) void act_long_rows_kernel(const ActArgs a) {
     for (int64_t at = (int64_t)threadIdx.x * kUnit; at < n; at += 1024 * kUnit) {
       // residual_out may be x or residual itself: each thread reads an
       // element again before it writes that element
-      typename E::unit h = load_part<E>(x, at, n, 0.0f), rv, wv;
-      if (add) rv = load_part<E>(res, at, n, 0.0f);
-      if (NORM) wv = load_part<E>(wt, at, n, 0.0f);
+      typename E::unit h = load_part<E, true, int64_t>(x, at, n, 0.0f), rv, wv;
+      if (add) rv = load_part<E, true, int64_t>(res, at, n, 0.0f);
+      if (NORM) wv = load_part<E, true, int64_t>(wt, at, n, 0.0f);
       float ss2 = 0.0f;
       uint32_t ab2 = 0;
       take_unit<E, NORM>(h, rv, wv, add, ss2, ab2);
-      if (NORM && a.residual_out) store_part<E>((raw *)a.residual_out + row * a.ldro, at, n, h);
-      give_unit<E, NORM>(a, row, at, h, wv, rs);
+      if (NORM && a.residual_out) store_part<E, int64_t>((raw *)a.residual_out + row * a.ldro, at, n, h);
+      give_unit<E, NORM, int64_t>(a, row, at, h, wv, rs);
     }
     if (a.q && threadIdx.x == 0) a.scale[row] = rs.scale;
   }

@@ -40,17 +40,25 @@ void launch_rows(const ActArgs &a, hipStream_t st) {
   hipLaunchKernelGGL((act_rows_kernel<E, NORM, TPR, U>), dim3((unsigned)grid), dim3(TPB), 0, st, a);
 }
 
+// The fewest threads that hold a row in two units each (fewer, later stores
+// overlap more rows' loads), measured on fp16 rows: 8192 x 1024 15.6 us with one
+// wave and two units, 18.9 with four waves and one; 8192 x 2048 23.7 with four
+// waves, 34 with eight; 4096 x 4096 24.4 / 25.5 / 34.6 with 256 x 2, 512 x 1,
+// 1024 x 1; 8192 x 8192 84 / 92 with 512 x 2, 1024 x 1.  Up to 16384 columns the
+// norm, with three units per eight elements, takes 1024 x 2 (2000 x 16384: 54
+// us, 512 x 4 64), the quantisation 512 x 4 (8000 x 11008: 51 us, 1024 x 2 60).
 template <typename E, bool NORM>
 void launch_act(const ActArgs &a, hipStream_t st) {
   const int64_t units = cdiv(a.cols, kUnit);
-  if (units <= 64) launch_rows<E, NORM, 64, 1>(a, st);
+  if (a.cols < kUnit || units > 4096)
+    hipLaunchKernelGGL((act_long_rows_kernel<E, NORM>), dim3((unsigned)std::min(a.rows, kMaxGrid)), dim3(1024), 0, st, a);
+  else if (units <= 64) launch_rows<E, NORM, 64, 1>(a, st);
+  else if (units <= 128) launch_rows<E, NORM, 64, 2>(a, st);
   else if (units <= 256) launch_rows<E, NORM, 256, 1>(a, st);
   else if (units <= 512) launch_rows<E, NORM, 256, 2>(a, st);
-  else if (units <= 1024) launch_rows<E, NORM, 256, 4>(a, st);
-  else if (units <= 2048) launch_rows<E, NORM, 1024, 2>(a, st);
-  else if (units <= 4096) launch_rows<E, NORM, 1024, 4>(a, st);
-  else
-    hipLaunchKernelGGL((act_long_rows_kernel<E, NORM>), dim3((unsigned)std::min(a.rows, kMaxGrid)), dim3(1024), 0, st, a);
+  else if (units <= 1024) launch_rows<E, NORM, 512, 2>(a, st);
+  else if (units <= 2048) launch_rows<E, NORM, NORM ? 1024 : 512, NORM ? 2 : 4>(a, st);
+  else launch_rows<E, NORM, 1024, 4>(a, st);
 }
 
 template <bool NORM>

@@ -44,7 +44,31 @@ struct HalfUnit {  // fp16 and bf16
   __device__ __forceinline__ void put(int i, uint16_t v) {
     w[i / 2] = i % 2 ? (w[i / 2] & 0xffffu) | (uint32_t)v << 16 : (w[i / 2] & 0xffff0000u) | v;
   }
+  // Drops the first n elements (0 .. 7) and fills up behind the rest.
+  __device__ __forceinline__ void drop(int n, uint16_t v) {
+    const uint32_t f = v | (uint32_t)v << 16;
+    if (n & 4) {
+      w[0] = w[2];
+      w[1] = w[3];
+      w[2] = w[3] = f;
+    }
+    if (n & 2) {
+      w[0] = w[1];
+      w[1] = w[2];
+      w[2] = w[3];
+      w[3] = f;
+    }
+    if (n & 1) {
+      w[0] = w[0] >> 16 | w[1] << 16;
+      w[1] = w[1] >> 16 | w[2] << 16;
+      w[2] = w[2] >> 16 | w[3] << 16;
+      w[3] = w[3] >> 16 | f << 16;
+    }
+  }
   __device__ __forceinline__ uint16_t at(int i) const { return (uint16_t)(w[i / 2] >> (16 * (i % 2))); }
+  // Keeps the unit as it is stored across this point: without it the compiler
+  // carries the converted values, twice the registers.
+  __device__ __forceinline__ void hold() { asm volatile("" : "+v"(w[0]), "+v"(w[1]), "+v"(w[2]), "+v"(w[3])); }
 };
 
 struct F16 {
@@ -85,7 +109,16 @@ struct FloatUnit {
     *reinterpret_cast<floats4 *>(p + 4) = floats4{f[4], f[5], f[6], f[7]};
   }
   __device__ __forceinline__ void put(int i, float v) { f[i] = v; }
+  __device__ __forceinline__ void drop(int n, float v) {
+#pragma unroll
+    for (int s = 4; s > 0; s /= 2)
+      if (n & s) {
+#pragma unroll
+        for (int i = 0; i < kUnit; ++i) f[i] = i + s < kUnit ? f[i + s] : v;
+      }
+  }
   __device__ __forceinline__ float at(int i) const { return f[i]; }
+  __device__ __forceinline__ void hold() {}
 };
 
 struct F32 {
@@ -95,23 +128,31 @@ struct F32 {
   static __device__ __forceinline__ raw round(float f) { return f; }
 };
 
-// The elements [at, at + 8) of a row of n: a whole unit, or the row's last
-// elements one by one with `fill` behind them (a fill for at >= n, too).
-template <typename E>
-__device__ __forceinline__ typename E::unit load_part(const typename E::raw *row, int64_t at, int64_t n, float fill) {
+// The elements [at, at + 8) of a row of n, with `fill` for those at n and
+// beyond, in two steps so that the first steps of several units are in flight
+// together: a row's last, incomplete unit is read eight elements from the
+// row's end and then moved into place.  Rows of less than eight elements (TINY)
+// are read one by one.  I is int for rows whose positions fit it (the row's
+// address then stays in scalar registers), else int64_t.
+template <typename E, bool TINY, typename I>
+__device__ __forceinline__ typename E::unit load_part(const typename E::raw *row, I at, I n, float fill) {
   typename E::unit u;
-  if (at + kUnit <= n) {
-    u.read(row + at);
-  } else {
-    u.fill(E::round(fill));
+  u.fill(E::round(fill));
+  if (TINY) {
 #pragma unroll
     for (int i = 0; i < kUnit; ++i)
       if (at + i < n) u.put(i, row[at + i]);
+  } else if (at < n) {
+    u.read(row + (at + kUnit <= n ? at : n - kUnit));
   }
   return u;
 }
-template <typename E>
-__device__ __forceinline__ void store_part(typename E::raw *row, int64_t at, int64_t n, const typename E::unit &u) {
+template <typename E, bool TINY, typename I>
+__device__ __forceinline__ void settle_part(typename E::unit &u, I at, I n, float fill) {
+  if (!TINY && at < n && at + kUnit > n) u.drop((int)(at + kUnit - n), E::round(fill));
+}
+template <typename E, typename I>
+__device__ __forceinline__ void store_part(typename E::raw *row, I at, I n, const typename E::unit &u) {
   if (at + kUnit <= n) {
     u.write(row + at);
   } else {

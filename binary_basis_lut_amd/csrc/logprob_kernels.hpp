@@ -76,14 +76,14 @@ __device__ __forceinline__ Stats shuffle(Stats a, int o) {
   return Stats{__shfl_xor(a.m, o), __shfl_xor(a.s, o), __shfl_xor(a.d, o)};
 }
 
+// What the waves of a workgroup share while they pick the best keys.
 struct LpShared {
   uint64_t cand[kLpCap];
-  uint64_t list[kLpMaxTop];  // the best keys so far, in order; 0 past their count
-  float tmax[kLpThreads];
+  uint64_t list[kLpMaxTop];  // the best keys, in order; 0 past their count
   Stats wave[kLpThreads / 64];
   uint64_t wkey[kLpThreads / 64];
+  float wthr[kLpThreads / 64];
   int count;
-  float thr;
 };
 
 // cand[0, n) -> the best top_k of them in list, in order.
@@ -112,6 +112,35 @@ __device__ __forceinline__ uint64_t block_max_key(LpShared &sh, uint64_t k) {
 #pragma unroll
   for (int i = 1; i < kLpThreads / 64; ++i) k = sh.wkey[i] > k ? sh.wkey[i] : k;
   return k;
+}
+
+// The largest value of the wave, in every lane.
+__device__ __forceinline__ float wave_max(float v) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
+  return v;
+}
+
+// The n-th largest (n >= 1) of the wave's values, -inf where fewer are above it.
+__device__ __forceinline__ float wave_nth(float v, int n) {
+  float m = wave_max(v);
+  while (--n > 0) {
+    const uint64_t at = __ballot(v == m);
+    if (v == m && (threadIdx.x % 64) == (unsigned)__builtin_ctzll(at)) v = kNegInf;
+    m = wave_max(v);
+  }
+  return m;
+}
+
+__device__ __forceinline__ Stats join_block(LpShared &sh, Stats st, float c) {
+#pragma unroll
+  for (int o = 32; o > 0; o >>= 1) st = join(st, shuffle(st, o), c);
+  if (threadIdx.x % 64 == 0) sh.wave[threadIdx.x / 64] = st;
+  __syncthreads();
+  st = sh.wave[0];
+#pragma unroll
+  for (int i = 1; i < kLpThreads / 64; ++i) st = join(st, sh.wave[i], c);
+  return st;
 }
 
 // Writes a row's results from its joined statistics and its ordered keys.
@@ -145,9 +174,23 @@ __host__ __device__ inline int64_t lp_part_bytes(int top_k) { return 16 + 8 * (i
 
 // One workgroup: one split of one row.  splits == 1 writes the row's results,
 // else the split's partial result goes to the workspace.
-template <typename E>
+//
+// Alternatives without sorting: the first slice gives a lower bound of the
+// top_k-th value (each wave's ceil(top_k / waves)-th largest thread maximum,
+// the least of them: at least top_k elements reach it), and only elements above
+// the bound become candidates in LDS.  After 2, 4, 8, ... slices the candidates
+// are reduced to the best top_k and the bound rises to the last of them, so
+// their number stays near top_k (1 + ln 2) however long the row is.  Equal
+// elements of later slices have higher indices and lose, hence "above".  Rows
+// that defeat this (long runs of equal logits, ascending rows, fewer than top_k
+// logits left unmasked) are taken again, one key at a time.
+//
+// Bound by the HBM read; the exponential, a quarter-rate instruction, is what
+// comes next (about 11 issue slots per element of which it takes four).
+template <typename E, bool TINY>
 __global__ __launch_bounds__(kLpThreads) void logprob_rows_kernel(const LogprobArgs a) {
   typedef typename E::raw raw;
+  constexpr int kWaves = kLpThreads / 64;
   __shared__ LpShared sh;
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x / a.splits;
@@ -156,22 +199,21 @@ __global__ __launch_bounds__(kLpThreads) void logprob_rows_kernel(const LogprobA
   const raw *x = (const raw *)a.logits + row * a.ld;
   const float c = a.scale * kLog2e;
   Stats st{kNegInf, 0.0f, 0.0f};
-  float thr = kNegInf;      // candidates are above it, or equal to it while `inclusive`
-  bool inclusive = true;
-  int have = 0;             // keys in the list
-  for (int at0 = begin; at0 < end; at0 += kLpSlice) {
+  float thr = kNegInf;
+  int slice = 0;
+  bool full = false;  // more candidates than LDS holds
+  if (tid == 0) sh.count = 0;
+  for (int at0 = begin; at0 < end; at0 += kLpSlice, ++slice) {
     typename E::unit v[kLpUnits];
-    const int units = min(kLpUnits, (end - at0 + kLpStep - 1) / kLpStep);
     float tm = kNegInf;
 #pragma unroll
-    for (int u = 0; u < kLpUnits; ++u) {
-      const int at = at0 + (u * kLpThreads + tid) * kUnit;
-      v[u] = load_part<E>(x, u < units ? at : end, end, kNegInf);
-    }
+    for (int u = 0; u < kLpUnits; ++u) v[u] = load_part<E, TINY, int>(x, at0 + (u * kLpThreads + tid) * kUnit, end, kNegInf);
 #pragma unroll
-    for (int u = 0; u < kLpUnits; ++u)
+    for (int u = 0; u < kLpUnits; ++u) {
+      settle_part<E, TINY, int>(v[u], at0 + (u * kLpThreads + tid) * kUnit, end, kNegInf);
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) tm = fmaxf(tm, v[u].get(i));
+    }
     {
       const float m = fmaxf(st.m, tm), M = ref(m);
       Stats now{m, 0.0f, 0.0f};
@@ -186,78 +228,60 @@ __global__ __launch_bounds__(kLpThreads) void logprob_rows_kernel(const LogprobA
       st = join(st, now, c);
     }
     if (a.top_k == 0) continue;
-    // A lower bound of the slice's top_k-th value: the top_k-th largest of the threads' maxima.
-    if (inclusive && have == 0) {
-      sh.tmax[tid] = tm;
-      if (tid == 0) sh.thr = kNegInf;
+    if (slice == 0) {
+      const float w = wave_nth(tm, (a.top_k + kWaves - 1) / kWaves);
+      if (tid % 64 == 0) sh.wthr[tid / 64] = w;
       __syncthreads();
-      int rank = 0;
-      for (int j = 0; j < kLpThreads; ++j) rank += sh.tmax[j] > tm || (sh.tmax[j] == tm && j < tid);
-      if (rank == a.top_k - 1) sh.thr = tm;
+      thr = sh.wthr[0];
+#pragma unroll
+      for (int i = 1; i < kWaves; ++i) thr = fminf(thr, sh.wthr[i]);
     }
-    if (tid < have) sh.cand[tid] = sh.list[tid];
-    if (tid == 0) sh.count = have;
-    __syncthreads();
-    if (inclusive && have == 0) thr = sh.thr;
-    auto is_cand = [&](int u, int i) {
-      const float f = v[u].get(i);
-      return at0 + (u * kLpThreads + tid) * kUnit + i < end && u < units && (f > thr || (inclusive && f == thr));
-    };
-    if (tm >= thr) {
+    if (!full && tm >= thr && tm > kNegInf) {
 #pragma unroll
       for (int u = 0; u < kLpUnits; ++u)
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i)
-          if (is_cand(u, i)) {
+        for (int i = 0; i < kUnit; ++i) {
+          const float f = v[u].get(i);
+          if (f > kNegInf && (f > thr || (slice == 0 && f == thr))) {
             const int p = atomicAdd(&sh.count, 1);
-            if (p < kLpCap) sh.cand[p] = key_of(v[u].get(i), at0 + (u * kLpThreads + tid) * kUnit + i);
+            if (p < kLpCap) sh.cand[p] = key_of(f, at0 + (u * kLpThreads + tid) * kUnit + i);
           }
-    }
-    __syncthreads();
-    const int n = sh.count;
-    if (n > have) {
-      if (n <= kLpCap) {
-        select_by_rank(sh, n, a.top_k);
-      } else {
-        // more candidates than LDS holds (long runs of equal logits): take the
-        // largest key below the last one, top_k times
-        uint64_t below = ~0ull;
-        if (tid < have) sh.cand[tid] = sh.list[tid];
-        __syncthreads();
-        const uint64_t mine = tid < have ? sh.cand[tid] : 0;
-        for (int j = 0; j < a.top_k; ++j) {
-          uint64_t best = mine < below ? mine : 0;
-#pragma unroll
-          for (int u = 0; u < kLpUnits; ++u)
-#pragma unroll
-            for (int i = 0; i < kUnit; ++i)
-              if (is_cand(u, i)) {
-                const uint64_t k = key_of(v[u].get(i), at0 + (u * kLpThreads + tid) * kUnit + i);
-                if (k < below && k > best) best = k;
-              }
-          below = block_max_key(sh, best);
-          if (tid == 0) sh.list[j] = below;
         }
-        __syncthreads();
-      }
-      have = min(n, a.top_k);
-      if (have == a.top_k) {
-        thr = value_of(sh.list[a.top_k - 1]);
-        inclusive = false;
-      }
     }
-    __syncthreads();
+    if (slice > 0 && (slice & (slice + 1)) == 0 && at0 + kLpSlice < end && !full) {
+      __syncthreads();
+      const int n = sh.count;
+      full = n > kLpCap;
+      if (!full && n >= a.top_k) {
+        select_by_rank(sh, n, a.top_k);
+        if (tid < a.top_k) sh.cand[tid] = sh.list[tid];
+        if (tid == 0) sh.count = a.top_k;
+        thr = value_of(sh.list[a.top_k - 1]);
+      }
+      __syncthreads();
+    }
   }
-  // join the threads' statistics
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) st = join(st, shuffle(st, o), c);
-  if (tid % 64 == 0) sh.wave[tid / 64] = st;
-  __syncthreads();
-  st = sh.wave[0];
-#pragma unroll
-  for (int i = 1; i < kLpThreads / 64; ++i) st = join(st, sh.wave[i], c);
-  if (tid >= have && tid < a.top_k) sh.list[tid] = 0;
-  __syncthreads();
+  st = join_block(sh, st, c);  // its barrier stands behind the last candidates, too
+  if (a.top_k > 0) {
+    const int n = sh.count;
+    if (!full && n >= a.top_k && n <= kLpCap) {
+      select_by_rank(sh, n, a.top_k);
+    } else {
+      // the largest key below the last one, top_k times
+      uint64_t below = ~0ull;
+      for (int j = 0; j < a.top_k; ++j) {
+        uint64_t best = 0;
+        for (int at = begin + tid; at < end; at += kLpThreads) {
+          const float f = E::load(x[at]);
+          const uint64_t k = key_of(f, at);
+          if (f == f && k < below && k > best) best = k;
+        }
+        below = block_max_key(sh, best);
+        if (tid == 0) sh.list[j] = below;
+      }
+      __syncthreads();
+    }
+  }
   if (a.splits == 1) {
     write_row<E>(a, row, st, sh.list);
   } else {
@@ -272,7 +296,7 @@ __global__ __launch_bounds__(kLpThreads) void logprob_rows_kernel(const LogprobA
   }
 }
 
-// Joins the splits of a row; splits * top_k keys, at most kLpMaxTop * kLpThreads.
+// Joins the splits of a row (at most kLpThreads of them).
 template <typename E>
 __global__ __launch_bounds__(kLpThreads) void logprob_join_kernel(const LogprobArgs a) {
   __shared__ LpShared sh;
@@ -281,20 +305,41 @@ __global__ __launch_bounds__(kLpThreads) void logprob_join_kernel(const LogprobA
   const uint8_t *base = a.workspace + row * a.splits * pb;
   const float c = a.scale * kLog2e;
   Stats st{kNegInf, 0.0f, 0.0f};
-  for (int i = 0; i < a.splits; ++i) {  // every thread the same, in order
-    const float *f = (const float *)(base + i * pb);
-    st = join(st, Stats{f[0], f[1], f[2]}, c);
-  }
-  // each split's list is in order: walk the heads of the lists, one list per thread
-  int head = 0;
+  uint64_t last = 0;  // the split's top_k-th key
   const uint64_t *list = (const uint64_t *)(base + (tid < a.splits ? tid : 0) * pb + 16);
-  for (int j = 0; j < a.top_k; ++j) {
-    const uint64_t k = tid < a.splits && head < a.top_k ? list[head] : 0;
-    const uint64_t best = block_max_key(sh, k);
-    if (k == best && k) ++head;
-    if (tid == 0) sh.list[j] = best;
+  if (tid < a.splits) {
+    const float *f = (const float *)(base + tid * pb);
+    st = Stats{f[0], f[1], f[2]};
+    if (a.top_k > 0) last = list[a.top_k - 1];
   }
-  __syncthreads();
+  if (tid == 0) sh.count = 0;
+  st = join_block(sh, st, c);
+  if (a.top_k > 0) {
+    // a split's top_k-th key bounds the row's from below: the largest of them
+    const uint64_t bound = block_max_key(sh, last);
+    for (int i = tid; i < a.splits * a.top_k; i += kLpThreads) {
+      const uint64_t k = ((const uint64_t *)(base + (i / a.top_k) * pb + 16))[i % a.top_k];
+      if (k >= bound && k > 0) {
+        const int p = atomicAdd(&sh.count, 1);
+        if (p < kLpCap) sh.cand[p] = k;
+      }
+    }
+    __syncthreads();
+    const int n = sh.count;
+    if (n <= kLpCap) {
+      select_by_rank(sh, n, a.top_k);
+    } else {
+      // each split's list is in order: the largest head, top_k times
+      int head = 0;
+      for (int j = 0; j < a.top_k; ++j) {
+        const uint64_t k = tid < a.splits && head < a.top_k ? list[head] : 0;
+        const uint64_t best = block_max_key(sh, k);
+        if (k == best && k) ++head;
+        if (tid == 0) sh.list[j] = best;
+      }
+      __syncthreads();
+    }
+  }
   write_row<E>(a, row, st, sh.list);
 }
 
