@@ -21,6 +21,7 @@ SOURCES = [CSRC / "fluxbin.hip"] + [CSRC / f"gemv_g{g}_rs{rs}_t{t}.hip" for g in
                                                       CSRC / "gemm_w8a8.hip", CSRC / "logprobs.hip"]
 HEADERS = [CSRC / "common.hpp", CSRC / "gemv_kernel.hpp", CSRC / "gemv_banked.hpp", CSRC / "aux_kernels.hpp",
            CSRC / "decomp_kernels.hpp", CSRC / "probes.hpp", CSRC / "status.hpp", CSRC / "elements.hpp",
+           CSRC / "wave_ops.hpp",
            CSRC / "act_kernels.hpp", CSRC / "gemm_w8a8_kernel.hpp", CSRC / "logprob_kernels.hpp", ROOT / "include" / "fluxbin.h"]
 DEPS = SOURCES + HEADERS
 BUILD = PKG / "_build"

@@ -15,6 +15,7 @@
 #pragma once
 
 #include "elements.hpp"
+#include "wave_ops.hpp"
 
 namespace fluxbin {
 
@@ -54,14 +55,6 @@ __device__ __forceinline__ RowScale row_scale(float ss, uint32_t abits, bool nor
 }
 
 __device__ __forceinline__ uint32_t abs_bits(float f) { return __builtin_bit_cast(uint32_t, f) & 0x7fffffffu; }
-
-__device__ __forceinline__ void wave_reduce(float &ss, uint32_t &ab) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    ss += __shfl_xor(ss, o);
-    ab = max(ab, (uint32_t)__shfl_xor((int)ab, o));
-  }
-}
 
 template <typename I>
 __device__ __forceinline__ void store_q(int8_t *row, I at, I n, const float (&t)[kUnit], const RowScale &r) {
@@ -167,7 +160,8 @@ __attribute__((amdgpu_waves_per_eu(TPR == 1024 && U <= 2 && sizeof(typename E::r
         wv[u].hold();
       }
     }
-    wave_reduce(ss, ab);
+    if (NORM) ss = wave_reduce<SumF>(ss);
+    ab = wave_reduce<MaxU>(ab);
     if (WPR > 1) {
       if (threadIdx.x % 64 == 0) {
         s_ss[threadIdx.x / 64] = ss;
@@ -214,7 +208,8 @@ __global__ __launch_bounds__(1024) void act_long_rows_kernel(const ActArgs a) {
       if (NORM) wv = load_part<E, true, int64_t>(wt, at, n, 0.0f);
       take_unit<E, NORM>(h, rv, wv, add, ss, ab);
     }
-    wave_reduce(ss, ab);
+    if (NORM) ss = wave_reduce<SumF>(ss);
+    ab = wave_reduce<MaxU>(ab);
     if (threadIdx.x % 64 == 0) {
       s_ss[threadIdx.x / 64] = ss;
       s_ab[threadIdx.x / 64] = ab;

@@ -18,6 +18,7 @@
 #pragma once
 
 #include "elements.hpp"
+#include "wave_ops.hpp"
 
 namespace fluxbin {
 
@@ -72,8 +73,15 @@ __device__ __forceinline__ float value_of(uint64_t key) {
 }
 __device__ __forceinline__ int index_of(uint64_t key) { return (int)~(uint32_t)key; }
 
-__device__ __forceinline__ Stats shuffle(Stats a, int o) {
-  return Stats{__shfl_xor(a.m, o), __shfl_xor(a.s, o), __shfl_xor(a.d, o)};
+// The joined statistics of a wave, in every lane: the largest x first, so that
+// each lane moves its own sums once.
+__device__ __forceinline__ Stats join_wave(Stats a, float c) {
+  Stats r;
+  r.m = wave_reduce<MaxF>(a.m);
+  const float t = a.m == kNegInf ? 0.0f : fmaxf((a.m - ref(r.m)) * c, -200.0f), f = __builtin_amdgcn_exp2f(t);
+  r.s = wave_reduce<SumF>(a.s * f);
+  r.d = wave_reduce<SumF>(fmaf(t, a.s, a.d) * f);
+  return r;
 }
 
 // What the waves of a workgroup share while they pick the best keys.
@@ -100,11 +108,7 @@ __device__ __forceinline__ void select_by_rank(LpShared &sh, int n, int top_k) {
 }
 
 __device__ __forceinline__ uint64_t block_max_key(LpShared &sh, uint64_t k) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) {
-    const uint64_t v = (uint64_t)__shfl_xor((unsigned long long)k, o);
-    k = v > k ? v : k;
-  }
+  k = wave_reduce<MaxKey>(k);
   __syncthreads();
   if (threadIdx.x % 64 == 0) sh.wkey[threadIdx.x / 64] = k;
   __syncthreads();
@@ -114,27 +118,19 @@ __device__ __forceinline__ uint64_t block_max_key(LpShared &sh, uint64_t k) {
   return k;
 }
 
-// The largest value of the wave, in every lane.
-__device__ __forceinline__ float wave_max(float v) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) v = fmaxf(v, __shfl_xor(v, o));
-  return v;
-}
-
 // The n-th largest (n >= 1) of the wave's values, -inf where fewer are above it.
 __device__ __forceinline__ float wave_nth(float v, int n) {
-  float m = wave_max(v);
+  float m = wave_reduce<MaxF>(v);
   while (--n > 0) {
     const uint64_t at = __ballot(v == m);
     if (v == m && (threadIdx.x % 64) == (unsigned)__builtin_ctzll(at)) v = kNegInf;
-    m = wave_max(v);
+    m = wave_reduce<MaxF>(v);
   }
   return m;
 }
 
 __device__ __forceinline__ Stats join_block(LpShared &sh, Stats st, float c) {
-#pragma unroll
-  for (int o = 32; o > 0; o >>= 1) st = join(st, shuffle(st, o), c);
+  st = join_wave(st, c);
   if (threadIdx.x % 64 == 0) sh.wave[threadIdx.x / 64] = st;
   __syncthreads();
   st = sh.wave[0];
@@ -143,10 +139,24 @@ __device__ __forceinline__ Stats join_block(LpShared &sh, Stats st, float c) {
   return st;
 }
 
-// Writes a row's results from its joined statistics and its ordered keys.
+// A row's target and its logit, fetched by thread 0 ahead of their use.
+struct Target {
+  int64_t index;
+  float x;
+};
+
 template <typename E>
-__device__ __forceinline__ void write_row(const LogprobArgs &a, int64_t row, Stats st, const uint64_t *list) {
-  typedef typename E::raw raw;
+__device__ __forceinline__ Target load_target(const LogprobArgs &a, int64_t row) {
+  Target t{-1, 0.0f};
+  if (a.targets && threadIdx.x == 0) {
+    t.index = a.targets[row];
+    if (t.index >= 0 && t.index < a.vocab) t.x = E::load(((const typename E::raw *)a.logits)[row * a.ld + t.index]);
+  }
+  return t;
+}
+
+// Writes a row's results from its joined statistics and its ordered keys.
+__device__ __forceinline__ void write_row(const LogprobArgs &a, int64_t row, Stats st, const uint64_t *list, Target target) {
   const float m = ref(st.m);
   const float l2 = __builtin_amdgcn_logf(st.s);  // S = 0 (nothing left): -inf
   const bool none = st.s == 0.0f;
@@ -154,10 +164,9 @@ __device__ __forceinline__ void write_row(const LogprobArgs &a, int64_t row, Sta
   const int t = threadIdx.x;
   if (t == 0) {
     if (a.targets) {
-      const int64_t target = a.targets[row];
       float v = 0.0f;  // a negative target is no target
-      if (target >= a.vocab) v = __builtin_nanf("");
-      else if (target >= 0) v = lp(E::load(((const raw *)a.logits)[row * a.ld + target]));
+      if (target.index >= a.vocab) v = __builtin_nanf("");
+      else if (target.index >= 0) v = lp(target.x);
       a.logprob[row] = v;
     }
     if (a.entropy) a.entropy[row] = none ? 0.0f : kLn2 * (l2 - st.d / st.s);
@@ -203,6 +212,7 @@ __global__ __launch_bounds__(kLpThreads) void logprob_rows_kernel(const LogprobA
   int slice = 0;
   bool full = false;  // more candidates than LDS holds
   if (tid == 0) sh.count = 0;
+  const Target target = a.splits == 1 ? load_target<E>(a, row) : Target{-1, 0.0f};
   for (int at0 = begin; at0 < end; at0 += kLpSlice, ++slice) {
     typename E::unit v[kLpUnits];
     float tm = kNegInf;
@@ -283,7 +293,7 @@ __global__ __launch_bounds__(kLpThreads) void logprob_rows_kernel(const LogprobA
     }
   }
   if (a.splits == 1) {
-    write_row<E>(a, row, st, sh.list);
+    write_row(a, row, st, sh.list, target);
   } else {
     uint8_t *p = a.workspace + (row * a.splits + split) * lp_part_bytes(a.top_k);
     if (tid == 0) {
@@ -304,6 +314,7 @@ __global__ __launch_bounds__(kLpThreads) void logprob_join_kernel(const LogprobA
   const int64_t row = blockIdx.x, pb = lp_part_bytes(a.top_k);
   const uint8_t *base = a.workspace + row * a.splits * pb;
   const float c = a.scale * kLog2e;
+  const Target target = load_target<E>(a, row);
   Stats st{kNegInf, 0.0f, 0.0f};
   uint64_t last = 0;  // the split's top_k-th key
   const uint64_t *list = (const uint64_t *)(base + (tid < a.splits ? tid : 0) * pb + 16);
@@ -340,7 +351,7 @@ __global__ __launch_bounds__(kLpThreads) void logprob_join_kernel(const LogprobA
       __syncthreads();
     }
   }
-  write_row<E>(a, row, st, sh.list);
+  write_row(a, row, st, sh.list, target);
 }
 
 }  // namespace fluxbin
