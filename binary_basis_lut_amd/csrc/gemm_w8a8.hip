@@ -1,5 +1,7 @@
 // gemm_w8a8.hip -- fluxbin_gemm_w8a8: argument checks, the choice of a kernel
 // instance, the launch.
+#include <algorithm>
+
 #include "gemm_w8a8_kernel.hpp"
 #include "status.hpp"
 
@@ -11,20 +13,63 @@ constexpr int64_t kMaxK = 131071;            // 131071 * 128 * 128 < 2^31
 constexpr int64_t kMaxMN = (int64_t)1 << 27;
 constexpr int64_t kTileStride = (int64_t)1 << 23;  // 256 strides stay below 2^31 (32-bit offsets)
 
-template <typename E, int BN, int BM, int WN, int WM, int S, int G>
+template <typename E, int BN, int BM, int WN, int WM, int WK, int KB, int S, int G>
 void launch_tile(const GemmArgs &g, hipStream_t st) {
-  hipLaunchKernelGGL((gemm_w8a8_tile_kernel<E, BN, BM, WN, WM, S, G>), dim3((unsigned)(cdiv(g.n, BN) * cdiv(g.m, BM))),
-                     dim3(64 * WN * WM), 0, st, g);
+  hipLaunchKernelGGL((gemm_w8a8_tile_kernel<E, BN, BM, WN, WM, WK, KB, S, G>),
+                     dim3((unsigned)(cdiv(g.n, BN) * cdiv(g.m, BM))), dim3(64 * WN * WM * WK), 0, st, g);
+}
+
+// Which tile: a workgroup's time is taken as the larger of its loads, at the 55
+// GB/s that one CU sustains on rows that come from HBM and the Infinity Cache,
+// and its products, at the 9 TOP/s of a CU (2.3 POP/s in all), and the CUs take
+// ceil(tiles / 256) workgroups one after another.  Measured (k x n = 4096 x 4096
+// unless said; us for the tiles 32 x 32, 32 x 64, 64 x 64, 64 x 128, 128 x 128,
+// 256 x 256, channels x tokens):
+//   64 tokens     8.6 / 10.4 / 13.0 / - / - / -
+//   128 tokens    - / 10.4 / 13.2 / 16.9 / - / -
+//   1024 tokens   - / - / - / 34.8 / 27.3 / 57.2
+//   64 tokens, 11008 x 16384     54.5 / - / 47.8 / - / - / -
+//   333 tokens, 11008 x 4096     - / - / 43.9 / 38.4 / 51.6 / -
+//   8192 tokens, 8192 x 28672    - / - / - / - / 2480 / 1850
+struct Tile {
+  int bn, bm;
+};
+constexpr Tile kTiles[] = {{32, 32}, {32, 64}, {64, 64}, {64, 128}, {128, 128}, {256, 256}};
+
+int pick_tile(const GemmArgs &g) {
+  int best = 0;
+  double least = 0;
+  for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
+    const Tile &t = kTiles[i];
+    const double rounds = (double)cdiv(cdiv(g.n, t.bn) * cdiv(g.m, t.bm), 256);
+    const double cost = rounds * std::max((t.bn + t.bm) / 55e9, 2.0 * t.bn * t.bm / 9e12);
+    if (i == 0 || cost < least) {
+      least = cost;
+      best = i;
+    }
+  }
+  return best;
 }
 
 template <typename E>
 void launch(const GemmArgs &g, hipStream_t st) {
-  const unsigned nb = (unsigned)cdiv(g.n, 16);
-  if (g.m <= 16) hipLaunchKernelGGL((gemm_w8a8_rows_kernel<E, 1, 4>), dim3(nb, 1), dim3(256), 0, st, g);
-  else if (g.m <= 64 || g.lda > kTileStride || g.ldw > kTileStride)
-    hipLaunchKernelGGL((gemm_w8a8_rows_kernel<E, 4, 4>), dim3(nb, (unsigned)cdiv(g.m, 64)), dim3(256), 0, st, g);
-  else if (g.m <= 1024) launch_tile<E, 64, 64, 2, 2, 4, 4>(g, st);
-  else launch_tile<E, 256, 256, 2, 4, 2, 1>(g, st);
+  // Up to 16 tokens each channel's weights go straight to registers: one token
+  // at 4096 x 4096 5.6 us (32 x 32 tiles: 7.6), at 8192 x 28672 40 (45), 16 tokens
+  // at 4096 x 4096 6.5 (7.9); but 16 tokens over 32000 channels 35 (31): there the
+  // tokens, read again by every 16 channels, cost as much as the weights.
+  if (g.m <= 4 || (g.m <= 16 && g.n <= 16384) || g.lda > kTileStride || g.ldw > kTileStride) {
+    hipLaunchKernelGGL((gemm_w8a8_rows_kernel<E, 8>), dim3((unsigned)cdiv(g.n, 16), (unsigned)cdiv(g.m, 16)), dim3(512), 0,
+                       st, g);
+    return;
+  }
+  switch (pick_tile(g)) {
+    case 0: launch_tile<E, 32, 32, 1, 1, 4, 256, 4, 2>(g, st); break;
+    case 1: launch_tile<E, 32, 64, 1, 2, 2, 256, 4, 4>(g, st); break;
+    case 2: launch_tile<E, 64, 64, 2, 2, 1, 128, 4, 4>(g, st); break;
+    case 3: launch_tile<E, 64, 128, 2, 4, 1, 128, 4, 4>(g, st); break;
+    case 4: launch_tile<E, 128, 128, 2, 4, 1, 128, 4, 2>(g, st); break;
+    default: launch_tile<E, 256, 256, 2, 4, 1, 128, 2, 1>(g, st); break;
+  }
 }
 
 }  // namespace

@@ -72,55 +72,46 @@ __device__ __forceinline__ i32x4 mask_tail(i32x4 v, int at, int k) {
   return v;
 }
 
-// One workgroup: 16 output channels x 16 MT tokens; its KW waves take blocks of
+// One workgroup: 16 output channels x 16 tokens; its KW waves take blocks of
 // 256 columns in turn and add their sums in LDS.  Both operands go from global
 // memory into the registers of v_mfma_i32_16x16x64_i8: lane l holds row l % 16
-// and, of each 64 columns, the 16 bytes from (l / 16) * 16 on.
-template <typename E, int MT, int KW>
+// and, of each 64 columns, the 16 bytes from (l / 16) * 16 on.  For one or a few
+// tokens the weights' HBM read is all there is to do (one token, 8192 x 28672:
+// 235 MB in 40 us = 5.9 TB/s), and eight waves a workgroup keep it going.
+template <typename E, int KW>
 __global__ __launch_bounds__(64 * KW) void gemm_w8a8_rows_kernel(const GemmArgs g) {
   constexpr int KB = 256;
-  __shared__ i32x4 part[KW][MT][64];
+  __shared__ i32x4 part[KW][64];
   const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
   const int r = lane % 16, c = lane / 16;
-  const int n0 = (int)blockIdx.x * 16, m0 = (int)blockIdx.y * 16 * MT;
+  const int n0 = (int)blockIdx.x * 16, m0 = (int)blockIdx.y * 16;
   const int last = (g.k - 1) / 16 * 16;  // the last 16-byte piece that a row has
   const int8_t *wr = g.w + (int64_t)min(n0 + r, g.n - 1) * g.ldw;
-  const int8_t *ar[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) ar[t] = g.a + (int64_t)min(m0 + 16 * t + r, g.m - 1) * g.lda;
-  i32x4 acc[MT];
-#pragma unroll
-  for (int t = 0; t < MT; ++t) acc[t] = i32x4{0, 0, 0, 0};
+  const int8_t *ar = g.a + (int64_t)min(m0 + r, g.m - 1) * g.lda;
+  i32x4 acc{0, 0, 0, 0};
   for (int kb = wave * KB; kb < g.k; kb += KW * KB) {
-    i32x4 wv[4], av[MT][4];
+    i32x4 wv[4], av[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j) {
-      const int at = kb + j * 64 + c * 16, from = min(at, last);
+      const int from = min(kb + j * 64 + c * 16, last);
       wv[j] = *reinterpret_cast<const i32x4 *>(wr + from);
-#pragma unroll
-      for (int t = 0; t < MT; ++t) av[t][j] = *reinterpret_cast<const i32x4 *>(ar[t] + from);
+      av[j] = *reinterpret_cast<const i32x4 *>(ar + from);
     }
     if (kb + KB > g.k) {
 #pragma unroll
-      for (int j = 0; j < 4; ++j)
-#pragma unroll
-        for (int t = 0; t < MT; ++t) av[t][j] = mask_tail(av[t][j], kb + j * 64 + c * 16, g.k);
+      for (int j = 0; j < 4; ++j) av[j] = mask_tail(av[j], kb + j * 64 + c * 16, g.k);
     }
 #pragma unroll
-    for (int j = 0; j < 4; ++j)
-#pragma unroll
-      for (int t = 0; t < MT; ++t) acc[t] = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[j], av[t][j], acc[t], 0, 0, 0);
+    for (int j = 0; j < 4; ++j) acc = __builtin_amdgcn_mfma_i32_16x16x64_i8(wv[j], av[j], acc, 0, 0, 0);
   }
-#pragma unroll
-  for (int t = 0; t < MT; ++t) part[wave][t][lane] = acc[t];
+  part[wave][lane] = acc;
   __syncthreads();
-  // lane l of a result tile holds channels 4 (l / 16) .. + 3 of token l % 16
-  for (int t = wave; t < MT; t += KW) {
-    i32x4 s = part[0][t][lane];
+  if (wave == 0) {
 #pragma unroll
-    for (int v = 1; v < KW; ++v) s += part[v][t][lane];
-    const int m = m0 + 16 * t + r;
-    store_outputs<E>(g, m, n0 + 4 * c, g.a_scale[min(m, g.m - 1)], load_channels(g, n0 + 4 * c), s);
+    for (int v = 1; v < KW; ++v) acc += part[v][lane];
+    // lane l holds channels 4 (l / 16) .. + 3 of token l % 16
+    const int m = m0 + r;
+    store_outputs<E>(g, m, n0 + 4 * c, g.a_scale[min(m, g.m - 1)], load_channels(g, n0 + 4 * c), acc);
   }
 }
 
@@ -152,30 +143,37 @@ __device__ __forceinline__ void wait_and_meet() {
   __builtin_amdgcn_sched_barrier(0);
 }
 
-// LDS-tiled product: BN channels x BM tokens per workgroup, WN x WM waves, 128
-// bytes of k per stage, S stages in LDS of which S - 1 are loaded ahead.  A
-// stage keeps each row's eight 16-byte pieces at positions exchanged by the
-// row's number (piece p of row r at p ^ (r / 2 % 8)), so that the 16 lanes of a
-// fragment read that the LDS serves at once, which take one piece of
-// consecutive rows, fall into all 64 banks; the exchange is made in the global
-// addresses, since a direct load writes LDS in lane order.
+// LDS-tiled product: BN channels x BM tokens per workgroup, WN x WM x WK waves
+// (WK of them share a wave tile and split each stage's k), KB bytes of k per
+// stage, S stages in LDS of which S - 1 are loaded ahead.  A stage keeps each
+// row's 16-byte pieces at positions exchanged by the row's number, so that the
+// 16 lanes of a fragment read that the LDS serves at once, which take one piece
+// of consecutive rows, fall into all 64 banks: piece p of row r stands at
+// p ^ (r / 2 % 8) in rows of 128 bytes and at p ^ (r % 16) in rows of 256.  The
+// exchange is made in the global addresses, since a direct load writes LDS in
+// lane order.
 //
-// Fragments are read one step ahead of the products; a step is G of a stage's
-// four 32-byte blocks of k.  Large wave tiles take G = 1 (a step's products
-// outlast the reads of the next), small ones the whole stage (G = 4), so that
-// a stage waits for LDS once and not four times.
-template <typename E, int BN, int BM, int WN, int WM, int S, int G>
-__global__ __launch_bounds__(64 * WN * WM) void gemm_w8a8_tile_kernel(const GemmArgs g) {
-  constexpr int KB = 128, W = WN * WM, STEPS = KB / 32 / G, STAGE = (BN + BM) * KB;
-  constexpr int NT = BN / WN / 32, MT = BM / WM / 32;  // 32 x 32 tiles of a wave
-  constexpr int LW = BN / 8 / W, LA = BM / 8 / W;      // direct loads (8 rows each) of a wave per stage
-  static_assert(BN % (8 * W) == 0 && BM % (8 * W) == 0, "rows divide over the waves");
+// Fragments are read one step ahead of the products; a step is G of the wave's
+// 32-byte blocks of a stage.  Large wave tiles take G = 1 (a step's products
+// outlast the reads of the next), small ones all their blocks at once, so that
+// a stage waits for LDS once.
+template <typename E, int BN, int BM, int WN, int WM, int WK, int KB, int S, int G>
+__global__ __launch_bounds__(64 * WN * WM * WK) void gemm_w8a8_tile_kernel(const GemmArgs g) {
+  constexpr int W = WN * WM * WK, BLOCKS = KB / 32 / WK, STEPS = BLOCKS / G, STAGE = (BN + BM) * KB;
+  constexpr int NT = BN / WN / 32, MT = BM / WM / 32;   // 32 x 32 tiles of a wave
+  constexpr int PIECES = KB / 16, RPL = 64 / PIECES;    // pieces of a row; rows of a direct load
+  constexpr int LW = BN / RPL / W, LA = BM / RPL / W;   // direct loads of a wave per stage
+  constexpr int PERIOD = 16 / RPL;                      // direct loads after which the exchange repeats
+  static_assert(KB == 128 || KB == 256, "rows of 8 or 16 pieces");
+  static_assert(BN % (RPL * W) == 0 && BM % (RPL * W) == 0, "rows divide over the waves");
+  static_assert(BLOCKS % G == 0 && STEPS > 0, "blocks divide into steps");
+  static_assert(WK == 1 || (WK - 1) * BN * BM * 4 <= S * STAGE, "the waves' sums fit the stages' memory");
   __shared__ __align__(1024) int8_t lds[S * STAGE];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   // Workgroups go to the 8 XCDs in turn: each XCD takes a contiguous eighth of
   // the tiles, in panels of kPanel token blocks, so that the workgroups that
   // share an L2 share operands.
-  constexpr int kPanel = 4;
+  constexpr int kPanel = BM >= 256 ? 4 : 8;
   const int nb = (g.n + BN - 1) / BN, mb = (g.m + BM - 1) / BM;
   int tile;
   {
@@ -191,36 +189,42 @@ __global__ __launch_bounds__(64 * WN * WM) void gemm_w8a8_tile_kernel(const Gemm
   const __amdgpu_buffer_rsrc_t from_w = buffer_of(g.w + n0 * g.ldw), from_a = buffer_of(g.a + m0 * g.lda);
   uint32_t off_w[LW], off_a[LA];
 #pragma unroll
-  for (int i = 0; i < LW; ++i) off_w[i] = (uint32_t)min((wave * LW + i) * 8 + lane / 8, g.n - 1 - n0) * (uint32_t)g.ldw;
+  for (int i = 0; i < LW; ++i) off_w[i] = (uint32_t)min((wave * LW + i) * RPL + lane / PIECES, g.n - 1 - n0) * (uint32_t)g.ldw;
 #pragma unroll
-  for (int i = 0; i < LA; ++i) off_a[i] = (uint32_t)min((wave * LA + i) * 8 + lane / 8, g.m - 1 - m0) * (uint32_t)g.lda;
+  for (int i = 0; i < LA; ++i) off_a[i] = (uint32_t)min((wave * LA + i) * RPL + lane / PIECES, g.m - 1 - m0) * (uint32_t)g.lda;
+  auto exchanged = [](int row, int p) { return KB == 128 ? p ^ (row / 2 % 8) : p ^ (row % 16); };
   auto fetch = [&](int stage, int8_t *buf) {
     const int k0 = stage * KB;
-    // the lane's piece in blocks of 8 rows of even and of odd number
-    uint32_t at[2];
+    uint32_t at[PERIOD];  // the lane's piece in the direct loads of number 0, 1, ...
 #pragma unroll
-    for (int odd = 0; odd < 2; ++odd) at[odd] = min(((lane % 8) ^ (4 * odd + lane / 16)) * 16, last - k0);
+    for (int j = 0; j < PERIOD; ++j) at[j] = min(exchanged(j * RPL + lane / PIECES, lane % PIECES) * 16, last - k0);
     FB_LDS int8_t *dst = (FB_LDS int8_t *)buf;
 #pragma unroll
-    for (int i = 0; i < LW; ++i) load_to_lds(from_w, off_w[i] + at[(wave * LW + i) % 2], k0, dst + (wave * LW + i) * 1024);
+    for (int i = 0; i < LW; ++i) {
+      const int j = wave * LW + i;
+      load_to_lds(from_w, off_w[i] + (LW % PERIOD == 0 ? at[i % PERIOD] : at[j % PERIOD]), k0, dst + j * 1024);
+    }
 #pragma unroll
-    for (int i = 0; i < LA; ++i)
-      load_to_lds(from_a, off_a[i] + at[(wave * LA + i) % 2], k0, dst + BN * KB + (wave * LA + i) * 1024);
+    for (int i = 0; i < LA; ++i) {
+      const int j = wave * LA + i;
+      load_to_lds(from_a, off_a[i] + (LA % PERIOD == 0 ? at[i % PERIOD] : at[j % PERIOD]), k0, dst + BN * KB + j * 1024);
+    }
   };
-  auto piece_at = [](int8_t *buf, int row, int p) {
-    return reinterpret_cast<i32x4 *>(buf + row * KB + ((p ^ (row / 2 % 8)) * 16));
+  auto piece_at = [&](int8_t *buf, int row, int p) {
+    return reinterpret_cast<i32x4 *>(buf + row * KB + exchanged(row, p) * 16);
   };
   const int stages = (g.k + KB - 1) / KB;
   // Where k ends inside a stage, the tokens' pieces behind it are cleared (what
   // the weights hold there is multiplied with these zeros).
   auto clear_tail = [&](int8_t *buf) {
     const int left = g.k - (stages - 1) * KB;
-    for (int i = threadIdx.x; i < BM * 8; i += 64 * W) {
-      i32x4 *at = piece_at(buf, BN + i / 8, i % 8);
-      if (i % 8 * 16 + 16 > left) *at = mask_tail(*at, i % 8 * 16, left);
+    for (int i = threadIdx.x; i < BM * PIECES; i += 64 * W) {
+      const int p = i % PIECES;
+      i32x4 *at = piece_at(buf, BN + i / PIECES, p);
+      if (p * 16 + 16 > left) *at = mask_tail(*at, p * 16, left);
     }
   };
-  const int wn = wave / WM, wm = wave % WM;
+  const int wk = wave % WK, wm = wave / WK % WM, wn = wave / WK / WM;
   const int r = lane % 32, half = lane / 32;
   i32x16 acc[NT][MT];
 #pragma unroll
@@ -231,7 +235,7 @@ __global__ __launch_bounds__(64 * WN * WM) void gemm_w8a8_tile_kernel(const Gemm
   auto load_step = [&](int8_t *buf, int s, int set) {
 #pragma unroll
     for (int b = 0; b < G; ++b) {
-      const int p = 2 * (s * G + b) + half;
+      const int p = 2 * (wk * BLOCKS + s * G + b) + half;
 #pragma unroll
       for (int i = 0; i < NT; ++i) wv[set][b][i] = *piece_at(buf, (wn * NT + i) * 32 + r, p);
 #pragma unroll
@@ -292,7 +296,7 @@ __global__ __launch_bounds__(64 * WN * WM) void gemm_w8a8_tile_kernel(const Gemm
     run_stage(t++, lds + slot * STAGE, lds + next * STAGE, first);
     slot = next;
   };
-  if (STEPS % 2) {  // a stage of one step: the sets take turns by stage
+  if (STEPS % 2) {  // an odd number of steps: the sets take turns by stage
     while (t + 2 < stages) {
       go(0);
       go(1);
@@ -314,6 +318,24 @@ __global__ __launch_bounds__(64 * WN * WM) void gemm_w8a8_tile_kernel(const Gemm
   for (int s = 0; s < STEPS; ++s) {
     if (s + 1 < STEPS) load_step(lds + slot * STAGE, s + 1, (s + 1) % 2);
     multiply(s % 2);
+  }
+  if (WK > 1) {  // the waves of a tile add their sums (exact, in any order)
+    wait_and_meet<0>();
+    i32x16 *sums = reinterpret_cast<i32x16 *>(lds);
+    const int pair = (wn * WM + wm) * NT * MT;
+#pragma unroll
+    for (int i = 0; i < NT; ++i)
+#pragma unroll
+      for (int j = 0; j < MT; ++j)
+        if (wk > 0) sums[((wk - 1) * WN * WM * NT * MT + pair + i * MT + j) * 64 + lane] = acc[i][j];
+    wait_and_meet<0>();
+    if (wk > 0) return;
+#pragma unroll
+    for (int v = 1; v < WK; ++v)
+#pragma unroll
+      for (int i = 0; i < NT; ++i)
+#pragma unroll
+        for (int j = 0; j < MT; ++j) acc[i][j] += sums[((v - 1) * WN * WM * NT * MT + pair + i * MT + j) * 64 + lane];
   }
   // The epilogue's addresses are not to be computed before the loop and held in
   // registers through it.
