@@ -44,6 +44,14 @@ struct HalfUnit {  // fp16 and bf16
   __device__ __forceinline__ void put(int i, uint16_t v) {
     w[i / 2] = i % 2 ? (w[i / 2] & 0xffffu) | (uint32_t)v << 16 : (w[i / 2] & 0xffff0000u) | v;
   }
+  // Element j of N units, for a j that differs between lanes.
+  template <int N>
+  static __device__ __forceinline__ float pick(const HalfUnit (&u)[N], int j) {
+    uint32_t v = 0;
+#pragma unroll
+    for (int i = 0; i < 4 * N; ++i) v = j / 2 == i ? u[i / 4].w[i % 4] : v;
+    return E::load((uint16_t)(v >> (16 * (j % 2))));
+  }
   // Drops the first n elements (0 .. 7) and fills up behind the rest.
   __device__ __forceinline__ void drop(int n, uint16_t v) {
     const uint32_t f = v | (uint32_t)v << 16;
@@ -109,6 +117,13 @@ struct FloatUnit {
     *reinterpret_cast<floats4 *>(p + 4) = floats4{f[4], f[5], f[6], f[7]};
   }
   __device__ __forceinline__ void put(int i, float v) { f[i] = v; }
+  template <int N>
+  static __device__ __forceinline__ float pick(const FloatUnit (&u)[N], int j) {
+    float v = 0.0f;
+#pragma unroll
+    for (int i = 0; i < kUnit * N; ++i) v = j == i ? u[i / kUnit].f[i % kUnit] : v;
+    return v;
+  }
   __device__ __forceinline__ void drop(int n, float v) {
 #pragma unroll
     for (int s = 4; s > 0; s /= 2)

@@ -38,9 +38,16 @@ constexpr int kLpUnits = 4;                                // units of eight per
 constexpr int kLpStep = kLpThreads * kUnit;                // columns of one unit of every thread
 constexpr int kLpSlice = kLpStep * kLpUnits;               // columns held in registers at a time
 constexpr int kLpMaxTop = 64;
+static_assert(kLpUnits * kUnit == 32, "a thread marks its elements of a slice in one word");
 constexpr int kLpCap = 512;                                // candidate keys that LDS holds
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_inff();
+
+// The next value above f (NaN above infinity: no value is as large).
+__device__ __forceinline__ float above(float f) {
+  const uint32_t b = __builtin_bit_cast(uint32_t, f + 0.0f);  // -0 counts as +0
+  return __builtin_bit_cast(float, (b >> 31) ? b - 1 : b + 1);
+}
 
 struct Stats {
   float m, s, d;  // largest x, sum of 2^(c (x - ref(m))), that sum weighted with its exponents
@@ -101,6 +108,7 @@ __device__ __forceinline__ void select_by_rank(LpShared &sh, int n, int top_k) {
   for (int i = threadIdx.x; i < n; i += kLpThreads) {
     const uint64_t k = sh.cand[i];
     int rank = 0;
+#pragma unroll 8
     for (int j = 0; j < n; ++j) rank += sh.cand[j] > k;
     if (rank < top_k) sh.list[rank] = k;
   }
@@ -139,20 +147,19 @@ __device__ __forceinline__ Stats join_block(LpShared &sh, Stats st, float c) {
   return st;
 }
 
-// A row's target and its logit, fetched by thread 0 ahead of their use.
+// A row's target and its logit, fetched by thread 0 ahead of their use (first
+// the index, with a row's other loads behind it, then the logit).
 struct Target {
   int64_t index;
   float x;
 };
 
+__device__ __forceinline__ Target target_index(const LogprobArgs &a, int64_t row) {
+  return Target{a.targets && threadIdx.x == 0 ? a.targets[row] : -1, 0.0f};
+}
 template <typename E>
-__device__ __forceinline__ Target load_target(const LogprobArgs &a, int64_t row) {
-  Target t{-1, 0.0f};
-  if (a.targets && threadIdx.x == 0) {
-    t.index = a.targets[row];
-    if (t.index >= 0 && t.index < a.vocab) t.x = E::load(((const typename E::raw *)a.logits)[row * a.ld + t.index]);
-  }
-  return t;
+__device__ __forceinline__ void target_logit(const LogprobArgs &a, int64_t row, Target &t) {
+  if (t.index >= 0 && t.index < a.vocab) t.x = E::load(((const typename E::raw *)a.logits)[row * a.ld + t.index]);
 }
 
 // Writes a row's results from its joined statistics and its ordered keys.
@@ -208,18 +215,20 @@ __global__ __launch_bounds__(kLpThreads) void logprob_rows_kernel(const LogprobA
   const raw *x = (const raw *)a.logits + row * a.ld;
   const float c = a.scale * kLog2e;
   Stats st{kNegInf, 0.0f, 0.0f};
-  float thr = kNegInf;
+  float thr = kNegInf, least = kNegInf;  // candidates are >= least
   int slice = 0;
   bool full = false;  // more candidates than LDS holds
   if (tid == 0) sh.count = 0;
-  const Target target = a.splits == 1 ? load_target<E>(a, row) : Target{-1, 0.0f};
+  Target target = a.splits == 1 ? target_index(a, row) : Target{-1, 0.0f};
   for (int at0 = begin; at0 < end; at0 += kLpSlice, ++slice) {
     typename E::unit v[kLpUnits];
+    const int units = min(kLpUnits, (end - at0 + kLpStep - 1) / kLpStep);  // units that hold columns
     float tm = kNegInf;
 #pragma unroll
     for (int u = 0; u < kLpUnits; ++u) v[u] = load_part<E, TINY, int>(x, at0 + (u * kLpThreads + tid) * kUnit, end, kNegInf);
 #pragma unroll
     for (int u = 0; u < kLpUnits; ++u) {
+      if (u >= units) break;
       settle_part<E, TINY, int>(v[u], at0 + (u * kLpThreads + tid) * kUnit, end, kNegInf);
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) tm = fmaxf(tm, v[u].get(i));
@@ -228,36 +237,43 @@ __global__ __launch_bounds__(kLpThreads) void logprob_rows_kernel(const LogprobA
       const float m = fmaxf(st.m, tm), M = ref(m);
       Stats now{m, 0.0f, 0.0f};
 #pragma unroll
-      for (int u = 0; u < kLpUnits; ++u)
+      for (int u = 0; u < kLpUnits; ++u) {
+        if (u >= units) break;
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) {
           const float d = (v[u].get(i) - M) * c, e = __builtin_amdgcn_exp2f(d);
           now.s += e;
           now.d = fmaf(e, fmaxf(d, -200.0f), now.d);
         }
+      }
       st = join(st, now, c);
     }
     if (a.top_k == 0) continue;
     if (slice == 0) {
-      const float w = wave_nth(tm, (a.top_k + kWaves - 1) / kWaves);
+      // of the waves that hold columns in every lane, or of the first
+      const int waves = max(1, min(kWaves, (end - begin) / (64 * kUnit)));
+      const float w = wave_nth(tm, (a.top_k + waves - 1) / waves);
       if (tid % 64 == 0) sh.wthr[tid / 64] = w;
       __syncthreads();
       thr = sh.wthr[0];
-#pragma unroll
-      for (int i = 1; i < kWaves; ++i) thr = fminf(thr, sh.wthr[i]);
+      for (int i = 1; i < waves; ++i) thr = fminf(thr, sh.wthr[i]);
+      least = fmaxf(thr, -3.402823466e38f);
     }
-    if (!full && tm >= thr && tm > kNegInf) {
+    if (!full && tm >= least) {
+      uint32_t mask = 0;  // element j of the slice's 32 at bit 31 - j
 #pragma unroll
       for (int u = 0; u < kLpUnits; ++u)
 #pragma unroll
-        for (int i = 0; i < kUnit; ++i) {
-          const float f = v[u].get(i);
-          if (f > kNegInf && (f > thr || (slice == 0 && f == thr))) {
-            const int p = atomicAdd(&sh.count, 1);
-            if (p < kLpCap) sh.cand[p] = key_of(f, at0 + (u * kLpThreads + tid) * kUnit + i);
-          }
-        }
+        for (int i = 0; i < kUnit; ++i) mask = mask + mask + (v[u].get(i) >= least ? 1u : 0u);
+      int p = atomicAdd(&sh.count, (int)__builtin_popcount(mask));
+      while (mask) {  // few
+        const int j = __builtin_clz(mask), at = at0 + ((j / kUnit) * kLpThreads + tid) * kUnit + j % kUnit;
+        mask &= ~(0x80000000u >> j);
+        if (p < kLpCap) sh.cand[p] = key_of(E::unit::pick(v, j), at);
+        ++p;
+      }
     }
+    if (slice == 0) least = above(thr);
     if (slice > 0 && (slice & (slice + 1)) == 0 && at0 + kLpSlice < end && !full) {
       __syncthreads();
       const int n = sh.count;
@@ -266,11 +282,12 @@ __global__ __launch_bounds__(kLpThreads) void logprob_rows_kernel(const LogprobA
         select_by_rank(sh, n, a.top_k);
         if (tid < a.top_k) sh.cand[tid] = sh.list[tid];
         if (tid == 0) sh.count = a.top_k;
-        thr = value_of(sh.list[a.top_k - 1]);
+        least = above(value_of(sh.list[a.top_k - 1]));
       }
       __syncthreads();
     }
   }
+  target_logit<E>(a, row, target);
   st = join_block(sh, st, c);  // its barrier stands behind the last candidates, too
   if (a.top_k > 0) {
     const int n = sh.count;
@@ -314,20 +331,26 @@ __global__ __launch_bounds__(kLpThreads) void logprob_join_kernel(const LogprobA
   const int64_t row = blockIdx.x, pb = lp_part_bytes(a.top_k);
   const uint8_t *base = a.workspace + row * a.splits * pb;
   const float c = a.scale * kLog2e;
-  const Target target = load_target<E>(a, row);
+  Target target = target_index(a, row);
   Stats st{kNegInf, 0.0f, 0.0f};
-  uint64_t last = 0;  // the split's top_k-th key
+  // Lower bounds of the row's top_k-th key: any split's top_k-th, and the least
+  // of the splits' ceil(top_k / splits)-th.
+  uint64_t last = 0, least = ~0ull;
   const uint64_t *list = (const uint64_t *)(base + (tid < a.splits ? tid : 0) * pb + 16);
   if (tid < a.splits) {
     const float *f = (const float *)(base + tid * pb);
     st = Stats{f[0], f[1], f[2]};
-    if (a.top_k > 0) last = list[a.top_k - 1];
+    if (a.top_k > 0) {
+      last = list[a.top_k - 1];
+      least = list[(a.top_k + a.splits - 1) / a.splits - 1];
+    }
   }
   if (tid == 0) sh.count = 0;
+  target_logit<E>(a, row, target);
   st = join_block(sh, st, c);
   if (a.top_k > 0) {
-    // a split's top_k-th key bounds the row's from below: the largest of them
-    const uint64_t bound = block_max_key(sh, last);
+    const uint64_t a_bound = block_max_key(sh, last), b_bound = ~block_max_key(sh, ~least);
+    const uint64_t bound = a_bound > b_bound ? a_bound : b_bound;
     for (int i = tid; i < a.splits * a.top_k; i += kLpThreads) {
       const uint64_t k = ((const uint64_t *)(base + (i / a.top_k) * pb + 16))[i % a.top_k];
       if (k >= bound && k > 0) {
