@@ -124,8 +124,16 @@ typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
 // base + soff + voff, lands at dst + 16 l.  A buffer load rather than a global
 // one: the compiler takes a direct global load for an LDS access too and would
 // then wait for all fragment reads in flight wherever it waits for some.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const int8_t *base) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>(base), 0, 0xffffffff, 0x00027000);
+// The same address, known to be the same in every lane: a buffer descriptor in
+// vector registers would be read out lane by lane around every load.
+__device__ __forceinline__ const int8_t *in_scalars(const int8_t *p) {
+  const uint64_t v = reinterpret_cast<uint64_t>(p);
+  return reinterpret_cast<const int8_t *>((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 |
+                                          (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
+}
+// A buffer of `bytes` 0 gives zeros and touches no memory.
+__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const int8_t *base, uint32_t bytes) {
+  return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>(base), 0, bytes, 0x00027000);
 }
 __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t base, uint32_t voff, uint32_t soff, FB_LDS int8_t *dst) {
   __builtin_amdgcn_raw_ptr_buffer_load_lds(base, (FB_LDS void *)dst, 16, voff, soff, 0, 0);
@@ -186,34 +194,34 @@ __global__ __launch_bounds__(64 * WN * WM * WK) void gemm_w8a8_tile_kernel(const
   const int last = (g.k - 1) / 16 * 16;
   // The loads' uniform bases and 32-bit offsets per lane (the host keeps 256
   // strides below 2^31); rows past the matrix repeat its last one.
-  const __amdgpu_buffer_rsrc_t from_w = buffer_of(g.w + n0 * g.ldw), from_a = buffer_of(g.a + m0 * g.lda);
+  const int8_t *base_w = in_scalars(g.w + n0 * g.ldw), *base_a = in_scalars(g.a + m0 * g.lda);
   uint32_t off_w[LW], off_a[LA];
 #pragma unroll
   for (int i = 0; i < LW; ++i) off_w[i] = (uint32_t)min((wave * LW + i) * RPL + lane / PIECES, g.n - 1 - n0) * (uint32_t)g.ldw;
 #pragma unroll
   for (int i = 0; i < LA; ++i) off_a[i] = (uint32_t)min((wave * LA + i) * RPL + lane / PIECES, g.m - 1 - m0) * (uint32_t)g.lda;
   auto exchanged = [](int row, int p) { return KB == 128 ? p ^ (row / 2 % 8) : p ^ (row % 16); };
-  auto fetch = [&](int stage, int8_t *buf) {
+  const int stages = (g.k + KB - 1) / KB;
+  // Direct load number i of the wave's LW + LA of a stage.  Loads of stages that
+  // do not exist read an empty buffer, so that every stage counts the same
+  // number of loads.
+  auto fetch = [&](int stage, int8_t *buf, int i) {
     const int k0 = stage * KB;
-    uint32_t at[PERIOD];  // the lane's piece in the direct loads of number 0, 1, ...
+    const uint32_t bytes = __builtin_amdgcn_readfirstlane(stage < stages ? -1 : 0);
+    const int j = i < LW ? wave * LW + i : wave * LA + i - LW;
+    // the lane's piece: the exchange repeats after PERIOD direct loads
+    const uint32_t at = min(exchanged(j % PERIOD * RPL + lane / PIECES, lane % PIECES) * 16, last - k0);
+    FB_LDS int8_t *dst = (FB_LDS int8_t *)buf + j * 1024;
+    if (i < LW) load_to_lds(buffer_of(base_w, bytes), off_w[i] + at, k0, dst);
+    else load_to_lds(buffer_of(base_a, bytes), off_a[i - LW] + at, k0, dst + BN * KB);
+  };
+  auto fetch_stage = [&](int stage, int8_t *buf) {
 #pragma unroll
-    for (int j = 0; j < PERIOD; ++j) at[j] = min(exchanged(j * RPL + lane / PIECES, lane % PIECES) * 16, last - k0);
-    FB_LDS int8_t *dst = (FB_LDS int8_t *)buf;
-#pragma unroll
-    for (int i = 0; i < LW; ++i) {
-      const int j = wave * LW + i;
-      load_to_lds(from_w, off_w[i] + (LW % PERIOD == 0 ? at[i % PERIOD] : at[j % PERIOD]), k0, dst + j * 1024);
-    }
-#pragma unroll
-    for (int i = 0; i < LA; ++i) {
-      const int j = wave * LA + i;
-      load_to_lds(from_a, off_a[i] + (LA % PERIOD == 0 ? at[i % PERIOD] : at[j % PERIOD]), k0, dst + BN * KB + j * 1024);
-    }
+    for (int i = 0; i < LW + LA; ++i) fetch(stage, buf, i);
   };
   auto piece_at = [&](int8_t *buf, int row, int p) {
     return reinterpret_cast<i32x4 *>(buf + row * KB + exchanged(row, p) * 16);
   };
-  const int stages = (g.k + KB - 1) / KB;
   // Where k ends inside a stage, the tokens' pieces behind it are cleared (what
   // the weights hold there is multiplied with these zeros).
   auto clear_tail = [&](int8_t *buf) {
@@ -251,19 +259,24 @@ __global__ __launch_bounds__(64 * WN * WM * WK) void gemm_w8a8_tile_kernel(const
         for (int j = 0; j < MT; ++j)
           acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[set][b][i], av[set][b][j], acc[i][j], 0, 0, 0);
   };
-  // Stage t + 1 has landed for every wave, and every wave has read stage t.
-  auto next_landed = [&](int t) {
-    if (t + S <= stages) wait_and_meet<(S - 2) * (LW + LA)>();  // the loads of S - 2 later stages may be in flight
-    else wait_and_meet<0>();
-    if (t + 2 == stages && g.k % KB) {
-      clear_tail(lds + (t + 1) % S * STAGE);
-      wait_and_meet<0>();
+  // The products of a step with a stage's loads between them: all loads at once
+  // would hold the wave until the memory pipe has taken them.
+  auto multiply_and_fetch = [&](int set, int stage, int8_t *buf) {
+    constexpr int PRODUCTS = G * NT * MT, L = LW + LA;
+#pragma unroll
+    for (int x = 0; x < PRODUCTS; ++x) {
+      const int b = x / (NT * MT), i = x / MT % NT, j = x % MT;
+#pragma unroll
+      for (int l = x * L / PRODUCTS; l < (x + 1) * L / PRODUCTS; ++l) fetch(stage, buf, l);
+      acc[i][j] = __builtin_amdgcn_mfma_i32_32x32x32_i8(wv[set][b][i], av[set][b][j], acc[i][j], 0, 0, 0);
+      __builtin_amdgcn_sched_barrier(0);
     }
   };
   // One stage that another follows; its first step's fragments are in set
   // `first`.  All reads of a step stand before the products of the step before,
-  // and the barrier that ends the stage's reads before the last step's
-  // products, which cover the first reads and the loads behind it.
+  // and the barrier that ends the stage's reads (and tells that the next stage
+  // has landed: the loads of S - 2 later ones may be in flight) before the last
+  // step's products, which cover the first reads and the loads behind it.
   auto run_stage = [&](int t, int8_t *cur, int8_t *nxt, int first) {
 #pragma unroll
     for (int s = 0; s + 1 < STEPS; ++s) {
@@ -273,21 +286,21 @@ __global__ __launch_bounds__(64 * WN * WM * WK) void gemm_w8a8_tile_kernel(const
       __builtin_amdgcn_sched_group_barrier(0x008, G * NT * MT, 0);    // products
       __builtin_amdgcn_sched_barrier(0);
     }
-    next_landed(t);
+    wait_and_meet<(S - 2) * (LW + LA)>();
+    if (t + 2 == stages && g.k % KB) {
+      clear_tail(nxt);
+      wait_and_meet<(S - 2) * (LW + LA)>();
+    }
     load_step(nxt, 0, (first + STEPS) % 2);
-    if (t + S < stages) fetch(t + S, cur);
     __builtin_amdgcn_sched_barrier(0);
-    multiply((first + STEPS - 1) % 2);
-    __builtin_amdgcn_sched_barrier(0);
+    multiply_and_fetch((first + STEPS - 1) % 2, t + S, cur);
   };
 #pragma unroll
-  for (int i = 0; i < S; ++i)
-    if (i < stages) fetch(i, lds + i * STAGE);
-  if (stages >= S) wait_and_meet<(S - 1) * (LW + LA)>();
-  else wait_and_meet<0>();
+  for (int i = 0; i < S; ++i) fetch_stage(i, lds + i * STAGE);
+  wait_and_meet<(S - 1) * (LW + LA)>();
   if (stages == 1 && g.k % KB) {
     clear_tail(lds);
-    wait_and_meet<0>();
+    wait_and_meet<(S - 1) * (LW + LA)>();
   }
   load_step(lds, 0, 0);
   int slot = 0, t = 0;
@@ -319,6 +332,7 @@ __global__ __launch_bounds__(64 * WN * WM * WK) void gemm_w8a8_tile_kernel(const
     if (s + 1 < STEPS) load_step(lds + slot * STAGE, s + 1, (s + 1) % 2);
     multiply(s % 2);
   }
+  __builtin_amdgcn_s_waitcnt(0);  // no direct load is in flight when the workgroup ends
   if (WK > 1) {  // the waves of a tile add their sums (exact, in any order)
     wait_and_meet<0>();
     i32x16 *sums = reinterpret_cast<i32x16 *>(lds);

@@ -252,6 +252,58 @@ def test_gemm_w8a8_types(fb, dt, m, n, k):
     gemm_case(fb, m, n, k, dt, bias=True)
 
 
+# (tokens, channels) of which each picks another tile: 32 x 64, 64 x 64, 64 x 128, 128 x 128, 256 x 256
+@pytest.mark.parametrize("m,n", [(61, 8190), (61, 16390), (333, 4093), (1030, 2050), (3500, 4499)])
+@pytest.mark.parametrize("k", [1, 16, 127, 128, 129, 256, 300, 513, 650])
+def test_gemm_w8a8_tiles(fb, m, n, k):
+    """Fewer stages than a tile holds, as many, and more, each with and without a tail of k."""
+    note(f"gemm_w8a8 tile {m} x {n} x {k}")
+    gemm_case(fb, m, n, k, "bf16" if k % 2 else "f16", bias=k > 200, ldy_pad=k % 2)
+
+
+def test_gemm_w8a8_wide_strides(fb):
+    """Row strides of more than 8 MiB, whose 256 rows pass 32-bit offsets."""
+    note("gemm_w8a8 strides of 2^23 + 16")
+    m, n, k, ld = 20, 40, 100, (1 << 23) + 16
+    g = torch.Generator().manual_seed(1)
+    a = torch.randint(-128, 128, (m, k), generator=g, dtype=torch.int8)
+    w = torch.randint(-128, 128, (n, k), generator=g, dtype=torch.int8)
+    ad, wd = strided(a, ld), strided(w, ld)
+    y = torch.empty((m, n), device="cuda")
+    one = torch.ones(max(m, n), device="cuda")
+    fb.fluxbin_gemm_w8a8(ad, ld, one, wd, ld, one, None, m, n, k, y, n, fb.DT_F32)
+    torch.cuda.synchronize()
+    assert torch.equal(y.cpu().double(), a.double() @ w.double().t())  # below 2^24: exact in fp32
+
+
+def test_outputs_beyond_32_bit_offsets(fb):
+    note("gemm_w8a8, quantize_rows and token_logprobs over more than 2^31 elements")
+    m, n, k = 40000, 60000, 64
+    g = torch.Generator(device="cuda").manual_seed(2)
+    a = torch.randint(-128, 128, (m, k), generator=g, dtype=torch.int8, device="cuda")
+    w = torch.randint(-128, 128, (n, k), generator=g, dtype=torch.int8, device="cuda")
+    sa, sw = torch.rand(m, generator=g, device="cuda") * 1e-3, torch.rand(n, generator=g, device="cuda") * 1e-2
+    y = torch.empty((m, n), dtype=torch.float16, device="cuda")
+    fb.fluxbin_gemm_w8a8(a, k, sa, w, k, sw, None, m, n, k, y, n, fb.DT_F16)
+    rows = torch.tensor([0, 1, 20000, 35791, 35792, 35793, m - 2, m - 1])
+    want = (a[rows].cpu().double() @ w.cpu().double().t()) * sa[rows].cpu().double()[:, None] * sw.cpu().double()
+    got = y[rows].cpu().double()
+    assert ((got - want).abs() <= (UNIT["f16"] + 5 * U) * want.abs() + TINY["f16"]).all()
+    q = torch.empty((m, n), dtype=torch.int8, device="cuda")
+    s = torch.empty(m, device="cuda")
+    fb.fluxbin_quantize_rows(y, n, fb.DT_F16, m, n, q, n, s)
+    q_want, _ = quant_oracle(y[rows].cpu().float().numpy())
+    assert np.array_equal(q[rows].cpu().numpy().astype(np.int64), q_want)
+    del q
+    top, idx = torch.empty((m, 3), device="cuda"), torch.empty((m, 3), dtype=torch.int64, device="cuda")
+    lp, ent = torch.empty(m, device="cuda"), torch.empty(m, device="cuda")
+    targets = torch.full((m,), n - 1, device="cuda")
+    assert fb.fluxbin_token_logprobs_workspace_size(m, n, 3) == 0
+    fb.fluxbin_token_logprobs(y, n, fb.DT_F16, m, n, 1.0, targets, lp, ent, 3, top, idx, None, 0)
+    check_scores(y[rows].cpu(), {"logprob": f64(lp[rows]), "entropy": f64(ent[rows]), "top": f64(top[rows]),
+                                 "index": idx[rows].cpu().numpy()}, 1.0, 3, targets[rows].cpu())
+
+
 @pytest.mark.parametrize("m", [1, 20, 70, 300])
 def test_gemm_w8a8_largest_sums(fb, m):
     """-128 * -128 over the longest k: every sum is 131071 * 2^14, just below 2^31."""
