@@ -10,6 +10,7 @@ using namespace fluxbin;
 namespace {
 
 constexpr int64_t kMaxK = 131071;            // 131071 * 128 * 128 < 2^31
+constexpr int64_t kCus = 256;                // compute units of an MI355X
 constexpr int64_t kMaxMN = (int64_t)1 << 27;
 constexpr int64_t kTileStride = (int64_t)1 << 23;  // 256 strides stay below 2^31 (32-bit offsets)
 
@@ -19,30 +20,40 @@ void launch_tile(const GemmArgs &g, hipStream_t st) {
                      dim3((unsigned)(cdiv(g.n, BN) * cdiv(g.m, BM))), dim3(64 * WN * WM * WK), 0, st, g);
 }
 
-// Which tile: a workgroup's time is taken as the larger of its loads, at the 55
-// GB/s that one CU sustains on rows that come from HBM and the Infinity Cache,
-// and its products, at the 9 TOP/s of a CU (2.3 POP/s in all), and the CUs take
-// ceil(tiles / 256) workgroups one after another.  Measured (k x n = 4096 x 4096
-// unless said; us for the tiles 32 x 32, 32 x 64, 64 x 64, 64 x 128, 128 x 128,
-// 256 x 256, channels x tokens):
-//   64 tokens     8.6 / 10.4 / 13.0 / - / - / -
-//   128 tokens    - / 10.4 / 13.2 / 16.9 / - / -
-//   1024 tokens   - / - / - / 34.8 / 27.3 / 57.2
-//   64 tokens, 11008 x 16384     54.5 / - / 47.8 / - / - / -
-//   333 tokens, 11008 x 4096     - / - / 43.9 / 38.4 / 51.6 / -
-//   8192 tokens, 8192 x 28672    - / - / - / - / 2480 / 1850
+// Which tile: a CU takes ceil(tiles / 256) of them, each for a fixed time (the
+// first loads' latency, the outputs) and a time per column of k, both fitted to
+// measurements.  Tiles of two stages leave room for several workgroups on a CU,
+// whose first loads and outputs overlap, and pay where there are more tiles than
+// CUs; the same tiles with four stages keep more loads in flight where there are
+// not.  Measured (us; tokens x channels x k):
+//                        32x32  32x64  64x64  64x128  128x128  two stages  256x256
+//   64 x 4096 x 4096       6.9    9.9   12.6     -       -          -         -
+//   64 x 16384 x 8192     48     46     33       -       -          -         -
+//   333 x 4096 x 11008     -      -     43      36      51          -         -
+//   1024 x 4096 x 4096     -      -      -      35      27         47        57
+//   3200 x 51200 x 144  1045      -    279     286     209        132       189
+//   4096 x 4096 x 512      -      -      -       -      25         21        24
+//   2000 x 8192 x 2000     -      -      -       -      69         59        48
+//   8192 x 28672 x 8192    -      -      -       -    2480          -      1740
+// (channels x tokens of a tile; "two stages" is 128 x 128; 64 x 64 with two:
+// 3200 x 51200 x 144 164.)
 struct Tile {
   int bn, bm;
+  bool many;         // for more tiles than CUs only
+  double fixed, per_k;  // us, ns
 };
-constexpr Tile kTiles[] = {{32, 32}, {32, 64}, {64, 64}, {64, 128}, {128, 128}, {256, 256}};
+constexpr Tile kTiles[] = {{32, 32, false, 0.8, 1.0},  {32, 64, false, 1.0, 1.7},   {64, 64, false, 1.0, 3.0},
+                           {64, 64, true, 0.5, 1.9},   {64, 128, false, 1.5, 3.0},  {128, 128, false, 2.5, 5.6},
+                           {128, 128, true, 2.0, 6.5}, {256, 256, false, 14.0, 15.7}};
 
 int pick_tile(const GemmArgs &g) {
   int best = 0;
   double least = 0;
   for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
     const Tile &t = kTiles[i];
-    const double rounds = (double)cdiv(cdiv(g.n, t.bn) * cdiv(g.m, t.bm), 256);
-    const double cost = rounds * std::max((t.bn + t.bm) / 55e9, 2.0 * t.bn * t.bm / 9e12);
+    const int64_t tiles = cdiv(g.n, t.bn) * cdiv(g.m, t.bm);
+    if (t.many && tiles <= kCus) continue;
+    const double cost = (double)cdiv(tiles, kCus) * (t.fixed * 1e3 + t.per_k * g.k);
     if (i == 0 || cost < least) {
       least = cost;
       best = i;
@@ -66,8 +77,10 @@ void launch(const GemmArgs &g, hipStream_t st) {
     case 0: launch_tile<E, 32, 32, 1, 1, 4, 256, 4, 2>(g, st); break;
     case 1: launch_tile<E, 32, 64, 1, 2, 2, 256, 4, 4>(g, st); break;
     case 2: launch_tile<E, 64, 64, 2, 2, 1, 128, 4, 4>(g, st); break;
-    case 3: launch_tile<E, 64, 128, 2, 4, 1, 128, 4, 4>(g, st); break;
-    case 4: launch_tile<E, 128, 128, 2, 4, 1, 128, 4, 2>(g, st); break;
+    case 3: launch_tile<E, 64, 64, 2, 2, 1, 128, 2, 4>(g, st); break;
+    case 4: launch_tile<E, 64, 128, 2, 4, 1, 128, 4, 4>(g, st); break;
+    case 5: launch_tile<E, 128, 128, 2, 4, 1, 128, 4, 2>(g, st); break;
+    case 6: launch_tile<E, 128, 128, 2, 4, 1, 128, 2, 2>(g, st); break;
     default: launch_tile<E, 256, 256, 2, 4, 1, 128, 2, 1>(g, st); break;
   }
 }

@@ -61,6 +61,28 @@ __device__ __forceinline__ void store_outputs(const GemmArgs &g, int m, int n0, 
   }
 }
 
+// Sixteen bytes of outputs, channels n .. of a row of `end`.
+__device__ __forceinline__ void store_piece(uint16_t *row, int n, int end, i32x4 v) {
+  if (n + 8 <= end) {
+    *reinterpret_cast<words4 *>(row + n) = words4{(uint32_t)v[0], (uint32_t)v[1], (uint32_t)v[2], (uint32_t)v[3]};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 8; ++i)
+      if (n + i < end) row[n + i] = (uint16_t)((uint32_t)v[i / 2] >> (16 * (i % 2)));
+  }
+}
+__device__ __forceinline__ void store_piece(float *row, int n, int end, i32x4 v) {
+  int w[4] = {v[0], v[1], v[2], v[3]};
+  if (n + 4 <= end) {
+    *reinterpret_cast<floats4 *>(row + n) = floats4{__builtin_bit_cast(float, w[0]), __builtin_bit_cast(float, w[1]),
+                                                    __builtin_bit_cast(float, w[2]), __builtin_bit_cast(float, w[3])};
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (n + i < end) row[n + i] = __builtin_bit_cast(float, w[i]);
+  }
+}
+
 // The bytes [at, at + 16) of a row's k, with zeros from k on.
 __device__ __forceinline__ i32x4 mask_tail(i32x4 v, int at, int k) {
 #pragma unroll
@@ -175,7 +197,7 @@ __global__ __launch_bounds__(64 * WN * WM * WK) void gemm_w8a8_tile_kernel(const
   static_assert(KB == 128 || KB == 256, "rows of 8 or 16 pieces");
   static_assert(BN % (RPL * W) == 0 && BM % (RPL * W) == 0, "rows divide over the waves");
   static_assert(BLOCKS % G == 0 && STEPS > 0, "blocks divide into steps");
-  static_assert(WK == 1 || (WK - 1) * BN * BM * 4 <= S * STAGE, "the waves' sums fit the stages' memory");
+  constexpr int sums_bytes = (WK - 1) * BN * BM * 4;    // what the waves of a tile hand to the first of them
   __shared__ __align__(1024) int8_t lds[S * STAGE];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   // Workgroups go to the 8 XCDs in turn: each XCD takes a contiguous eighth of
@@ -335,7 +357,7 @@ __global__ __launch_bounds__(64 * WN * WM * WK) void gemm_w8a8_tile_kernel(const
   __builtin_amdgcn_s_waitcnt(0);  // no direct load is in flight when the workgroup ends
   if (WK > 1) {  // the waves of a tile add their sums (exact, in any order)
     wait_and_meet<0>();
-    i32x16 *sums = reinterpret_cast<i32x16 *>(lds);
+    i32x16 *sums = reinterpret_cast<i32x16 *>(lds);  // the first sums_bytes of the stages' memory
     const int pair = (wn * WM + wm) * NT * MT;
 #pragma unroll
     for (int i = 0; i < NT; ++i)
@@ -351,26 +373,50 @@ __global__ __launch_bounds__(64 * WN * WM * WK) void gemm_w8a8_tile_kernel(const
 #pragma unroll
         for (int j = 0; j < MT; ++j) acc[i][j] += sums[((v - 1) * WN * WM * NT * MT + pair + i * MT + j) * 64 + lane];
   }
-  // The epilogue's addresses are not to be computed before the loop and held in
-  // registers through it.
-  int ne = n0 + wn * NT * 32 + 4 * half, me = m0 + wm * MT * 32 + r;
-  asm volatile("" : "+v"(ne), "+v"(me));
-  // lane l of a result tile holds token l % 32, channels 8 q + 4 (l / 32) .. + 3
-  float sa[MT];
+  // Outputs.  A lane holds four channels of one token at a time; stored as they
+  // are, 32 rows would be touched 16 bytes each.  So a wave turns 32 tokens x 32 C
+  // channels at a time in a piece of LDS of its own and stores up to 128
+  // consecutive bytes of a row.
+  typedef typename E::raw raw;
+  constexpr int C = NT >= 2 && sizeof(raw) == 2 ? 2 : 1, COLS = 32 * C, PITCH = COLS + 16 / (int)sizeof(raw);
+  constexpr int PER = 16 / (int)sizeof(raw), LANES = COLS / PER;  // channels of a 16-byte piece; pieces of a row
+  constexpr int TILES = (WK > 1 ? WN * WM : W);
+  static_assert(NT % C == 0 && sums_bytes + TILES * 32 * PITCH * (int)sizeof(raw) <= S * STAGE, "the turned tiles fit the stages' memory");
+  if (WK == 1) wait_and_meet<0>();  // every wave has read its last fragments
+  else __builtin_amdgcn_s_waitcnt(0);
+  // (the addresses are not to be computed before the loop and held through it)
+  int ne = n0 + wn * NT * 32, me = m0 + wm * MT * 32;
+  asm volatile("" : "+s"(ne), "+s"(me));
+  raw *out = reinterpret_cast<raw *>(lds + (WK > 1 ? sums_bytes : 0)) + (wn * WM + wm) * 32 * PITCH;
 #pragma unroll
-  for (int j = 0; j < MT; ++j) sa[j] = g.a_scale[min(me + j * 32, g.m - 1)];
+  for (int j = 0; j < MT; ++j) {
+    const float sa = g.a_scale[min(me + j * 32 + r, g.m - 1)];
 #pragma unroll
-  for (int i = 0; i < NT; ++i)
+    for (int i0 = 0; i0 < NT; i0 += C) {
+      // lane l of a 32 x 32 tile holds token l % 32, channels 8 q + 4 (l / 32) .. + 3
 #pragma unroll
-    for (int q = 0; q < 4; ++q) {
-      const int n = ne + i * 32 + 8 * q;
-      const Channels c = load_channels(g, n);
+      for (int i = i0; i < i0 + C; ++i)
 #pragma unroll
-      for (int j = 0; j < MT; ++j)
-        store_outputs<E>(g, me + j * 32, n, sa[j], c,
-                         i32x4{acc[i][j][4 * q], acc[i][j][4 * q + 1], acc[i][j][4 * q + 2], acc[i][j][4 * q + 3]});
-      __builtin_amdgcn_sched_barrier(0);
+        for (int q = 0; q < 4; ++q) {
+          const Channels c = load_channels(g, ne + i * 32 + 8 * q + 4 * half);
+          raw v[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) v[e] = E::round((float)acc[i][j][4 * q + e] * sa * c.scale[e] + c.bias[e]);
+          put4(out + r * PITCH + (i - i0) * 32 + 8 * q + 4 * half, v);
+          if (NT > 2) __builtin_amdgcn_sched_barrier(0);  // (few registers are left beside a large tile's sums)
+        }
+      __builtin_amdgcn_wave_barrier();
+#pragma unroll
+      for (int p = 0; p < 32 * LANES / 64; ++p) {
+        const int row = (p * 64 + lane) / LANES, col = lane % LANES * PER;
+        const i32x4 v = *reinterpret_cast<const i32x4 *>(out + row * PITCH + col);
+        const int m = me + j * 32 + row, n = ne + i0 * 32 + col;
+        if (m < g.m) store_piece((raw *)g.y + (int64_t)m * g.ldy, n, g.n, v);
+      }
+      __builtin_amdgcn_wave_barrier();
+      if (NT > 2) __builtin_amdgcn_sched_barrier(0);
     }
+  }
 }
 
 }  // namespace fluxbin
