@@ -128,6 +128,13 @@ __device__ __forceinline__ uint64_t block_max_key(LpShared &sh, uint64_t k) {
 
 // The n-th largest (n >= 1) of the wave's values, -inf where fewer are above it.
 __device__ __forceinline__ float wave_nth(float v, int n) {
+  if (n > 4) {  // by the number of larger values, 64 independent comparisons
+    int larger = 0;
+#pragma unroll
+    for (int j = 0; j < 64; ++j)
+      larger += __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, v), j)) > v;
+    return -wave_reduce<MaxF>(larger < n ? -v : kNegInf);  // the least of those with fewer than n above them
+  }
   float m = wave_reduce<MaxF>(v);
   while (--n > 0) {
     const uint64_t at = __ballot(v == m);
@@ -201,12 +208,16 @@ __host__ __device__ inline int64_t lp_part_bytes(int top_k) { return 16 + 8 * (i
 // that defeat this (long runs of equal logits, ascending rows, fewer than top_k
 // logits left unmasked) are taken again, one key at a time.
 //
+// SMALL (splits of at most kLpStep columns): a thread takes single columns, 256
+// apart, instead of eight in a row, so that all threads have their part of a
+// short row and its bound is close.
+//
 // Bound by the HBM read; the exponential, a quarter-rate instruction, is what
 // comes next (about 11 issue slots per element of which it takes four).
-template <typename E, bool TINY>
+template <typename E, bool SMALL>
 __global__ __launch_bounds__(kLpThreads) void logprob_rows_kernel(const LogprobArgs a) {
   typedef typename E::raw raw;
-  constexpr int kWaves = kLpThreads / 64;
+  constexpr int kWaves = kLpThreads / 64, U = SMALL ? 1 : kLpUnits;
   __shared__ LpShared sh;
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x / a.splits;
@@ -221,15 +232,22 @@ __global__ __launch_bounds__(kLpThreads) void logprob_rows_kernel(const LogprobA
   if (tid == 0) sh.count = 0;
   Target target = a.splits == 1 ? target_index(a, row) : Target{-1, 0.0f};
   for (int at0 = begin; at0 < end; at0 += kLpSlice, ++slice) {
-    typename E::unit v[kLpUnits];
-    const int units = min(kLpUnits, (end - at0 + kLpStep - 1) / kLpStep);  // units that hold columns
+    typename E::unit v[U];
+    const int units = min(U, (end - at0 + kLpStep - 1) / kLpStep);  // units that hold columns
     float tm = kNegInf;
+    if (SMALL) {
+      v[0].fill(E::round(kNegInf));
 #pragma unroll
-    for (int u = 0; u < kLpUnits; ++u) v[u] = load_part<E, TINY, int>(x, at0 + (u * kLpThreads + tid) * kUnit, end, kNegInf);
+      for (int i = 0; i < kUnit; ++i)
+        if (at0 + i * kLpThreads + tid < end) v[0].put(i, x[at0 + i * kLpThreads + tid]);
+    } else {
 #pragma unroll
-    for (int u = 0; u < kLpUnits; ++u) {
+      for (int u = 0; u < U; ++u) v[u] = load_part<E, false, int>(x, at0 + (u * kLpThreads + tid) * kUnit, end, kNegInf);
+    }
+#pragma unroll
+    for (int u = 0; u < U; ++u) {
       if (u >= units) break;
-      settle_part<E, TINY, int>(v[u], at0 + (u * kLpThreads + tid) * kUnit, end, kNegInf);
+      if (!SMALL) settle_part<E, false, int>(v[u], at0 + (u * kLpThreads + tid) * kUnit, end, kNegInf);
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) tm = fmaxf(tm, v[u].get(i));
     }
@@ -237,7 +255,7 @@ __global__ __launch_bounds__(kLpThreads) void logprob_rows_kernel(const LogprobA
       const float m = fmaxf(st.m, tm), M = ref(m);
       Stats now{m, 0.0f, 0.0f};
 #pragma unroll
-      for (int u = 0; u < kLpUnits; ++u) {
+      for (int u = 0; u < U; ++u) {
         if (u >= units) break;
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) {
@@ -251,7 +269,7 @@ __global__ __launch_bounds__(kLpThreads) void logprob_rows_kernel(const LogprobA
     if (a.top_k == 0) continue;
     if (slice == 0) {
       // of the waves that hold columns in every lane, or of the first
-      const int waves = max(1, min(kWaves, (end - begin) / (64 * kUnit)));
+      const int waves = max(1, min(kWaves, (end - begin) / (64 * (SMALL ? 1 : kUnit))));
       const float w = wave_nth(tm, (a.top_k + waves - 1) / waves);
       if (tid % 64 == 0) sh.wthr[tid / 64] = w;
       __syncthreads();
@@ -260,15 +278,16 @@ __global__ __launch_bounds__(kLpThreads) void logprob_rows_kernel(const LogprobA
       least = fmaxf(thr, -3.402823466e38f);
     }
     if (!full && tm >= least) {
-      uint32_t mask = 0;  // element j of the slice's 32 at bit 31 - j
+      uint32_t mask = 0;  // element j of the slice's 8 U at bit 8 U - 1 - j
 #pragma unroll
-      for (int u = 0; u < kLpUnits; ++u)
+      for (int u = 0; u < U; ++u)
 #pragma unroll
         for (int i = 0; i < kUnit; ++i) mask = mask + mask + (v[u].get(i) >= least ? 1u : 0u);
       int p = atomicAdd(&sh.count, (int)__builtin_popcount(mask));
       while (mask) {  // few
-        const int j = __builtin_clz(mask), at = at0 + ((j / kUnit) * kLpThreads + tid) * kUnit + j % kUnit;
-        mask &= ~(0x80000000u >> j);
+        const int j = __builtin_clz(mask) - (32 - kUnit * U);
+        const int at = at0 + (SMALL ? j * kLpThreads + tid : ((j / kUnit) * kLpThreads + tid) * kUnit + j % kUnit);
+        mask &= ~(1u << (kUnit * U - 1 - j));
         if (p < kLpCap) sh.cand[p] = key_of(E::unit::pick(v, j), at);
         ++p;
       }
@@ -333,24 +352,27 @@ __global__ __launch_bounds__(kLpThreads) void logprob_join_kernel(const LogprobA
   const float c = a.scale * kLog2e;
   Target target = target_index(a, row);
   Stats st{kNegInf, 0.0f, 0.0f};
-  // Lower bounds of the row's top_k-th key: any split's top_k-th, and the least
-  // of the splits' ceil(top_k / splits)-th.
-  uint64_t last = 0, least = ~0ull;
+  // A lower bound of the row's top_k-th key: with t = ceil(top_k / splits), the
+  // ceil(top_k / t)-th largest of the splits' t-th keys (each has t keys from it on).
+  uint64_t mine = 0;
+  const int t = a.top_k > 0 ? (a.top_k + a.splits - 1) / a.splits : 1;
   const uint64_t *list = (const uint64_t *)(base + (tid < a.splits ? tid : 0) * pb + 16);
   if (tid < a.splits) {
     const float *f = (const float *)(base + tid * pb);
     st = Stats{f[0], f[1], f[2]};
-    if (a.top_k > 0) {
-      last = list[a.top_k - 1];
-      least = list[(a.top_k + a.splits - 1) / a.splits - 1];
-    }
+    if (a.top_k > 0) mine = list[t - 1];
+    sh.cand[tid] = mine;
   }
   if (tid == 0) sh.count = 0;
   target_logit<E>(a, row, target);
   st = join_block(sh, st, c);
   if (a.top_k > 0) {
-    const uint64_t a_bound = block_max_key(sh, last), b_bound = ~block_max_key(sh, ~least);
-    const uint64_t bound = a_bound > b_bound ? a_bound : b_bound;
+    int rank = 0;
+#pragma unroll 8
+    for (int i = 0; i < a.splits; ++i) rank += sh.cand[i] > mine || (sh.cand[i] == mine && i < tid);
+    if (tid < a.splits && rank == (a.top_k + t - 1) / t - 1) sh.wkey[0] = mine;
+    __syncthreads();
+    const uint64_t bound = sh.wkey[0];
     for (int i = tid; i < a.splits * a.top_k; i += kLpThreads) {
       const uint64_t k = ((const uint64_t *)(base + (i / a.top_k) * pb + 16))[i % a.top_k];
       if (k >= bound && k > 0) {

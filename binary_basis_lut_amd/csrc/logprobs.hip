@@ -48,7 +48,7 @@ size_t ws_bytes(int64_t rows, const LpPlan &p, int32_t top_k) {
 template <typename E>
 void launch(const LogprobArgs &a, hipStream_t st) {
   const dim3 grid((unsigned)(a.rows * a.splits)), block(kLpThreads);
-  if (a.vocab < kUnit) hipLaunchKernelGGL((logprob_rows_kernel<E, true>), grid, block, 0, st, a);
+  if (a.split_len <= kLpStep) hipLaunchKernelGGL((logprob_rows_kernel<E, true>), grid, block, 0, st, a);
   else hipLaunchKernelGGL((logprob_rows_kernel<E, false>), grid, block, 0, st, a);
   if (a.splits > 1) hipLaunchKernelGGL(logprob_join_kernel<E>, dim3((unsigned)a.rows), dim3(kLpThreads), 0, st, a);
 }
