@@ -20,40 +20,48 @@ void launch_tile(const GemmArgs &g, hipStream_t st) {
                      dim3((unsigned)(cdiv(g.n, BN) * cdiv(g.m, BM))), dim3(64 * WN * WM * WK), 0, st, g);
 }
 
-// Which tile: a CU takes ceil(tiles / 256) of them, each for a fixed time (the
-// first loads' latency, the outputs) and a time per column of k, both fitted to
-// measurements.  Tiles of two stages leave room for several workgroups on a CU,
-// whose first loads and outputs overlap, and pay where there are more tiles than
-// CUs; the same tiles with four stages keep more loads in flight where there are
-// not.  Measured (us; tokens x channels x k):
-//                        32x32  32x64  64x64  64x128  128x128  two stages  256x256
-//   64 x 4096 x 4096       6.9    9.9   12.6     -       -          -         -
-//   64 x 16384 x 8192     48     46     33       -       -          -         -
-//   333 x 4096 x 11008     -      -     43      36      51          -         -
-//   1024 x 4096 x 4096     -      -      -      35      27         47        57
-//   3200 x 51200 x 144  1045      -    279     286     209        132       189
-//   4096 x 4096 x 512      -      -      -       -      25         21        24
-//   2000 x 8192 x 2000     -      -      -       -      69         59        48
-//   8192 x 28672 x 8192    -      -      -       -    2480          -      1740
-// (channels x tokens of a tile; "two stages" is 128 x 128; 64 x 64 with two:
-// 3200 x 51200 x 144 164.)
+// Which kernel and tile (channels x tokens): a CU takes ceil(tiles / 256) of them,
+// each for a fixed time (the first loads' latency, the outputs) and a time per
+// column of k, both fitted to measurements.  16 x 16 is the kernel without LDS
+// stages; its tokens come from the caches and cost by their number.  Tiles of
+// two stages leave room for several workgroups on a CU, whose first loads and
+// outputs overlap, and pay where there are more tiles than CUs; the same tiles
+// with four stages keep more loads in flight where there are not.  Measured
+// (us, weights from HBM; tokens x channels x k):
+//                      16x16 32x32 64x32 32x64 64x64 64x128 128x128 same, two 256x256
+//   1 x 4096 x 4096       5.6   7.6    -     -     -     -      -        -       -
+//   1 x 57344 x 8192       74    88    -     -     -     -      -        -       -
+//   16 x 8192 x 8192       19    15   20     -     -     -      -        -       -
+//   16 x 32000 x 4096      36    31   28     -     -     -      -        -       -
+//   64 x 4096 x 4096        -   6.9    -   9.9    13     -      -        -       -
+//   64 x 16384 x 8192       -    48   42    45    33    37      -        -       -
+//   128 x 16384 x 8192      -     -   63    66    49    40     49       70       -
+//   333 x 4096 x 11008      -     -    -     -    43    36     51        -       -
+//   200 x 57344 x 4096      -     -    -     -   119   113     98       91       -
+//   1024 x 4096 x 4096      -     -    -     -     -    35     27       47      57
+//   3200 x 51200 x 144      -  1045    -     -   279   286    209      132     189
+//   4096 x 4096 x 512       -     -    -     -     -     -     25       21      24
+//   2000 x 8192 x 2000      -     -    -     -     -     -     69       59      48
+//   8192 x 28672 x 8192     -     -    -     -     -     -   2480        -    1740
 struct Tile {
   int bn, bm;
-  bool many;         // for more tiles than CUs only
+  bool many;            // for more tiles than CUs only
   double fixed, per_k;  // us, ns
 };
-constexpr Tile kTiles[] = {{32, 32, false, 0.8, 1.0},  {32, 64, false, 1.0, 1.7},   {64, 64, false, 1.0, 3.0},
-                           {64, 64, true, 0.5, 1.9},   {64, 128, false, 1.5, 3.0},  {128, 128, false, 2.5, 5.6},
-                           {128, 128, true, 2.0, 6.5}, {256, 256, false, 14.0, 15.7}};
+constexpr Tile kTiles[] = {{16, 16, false, 0.3, 0.6},  {32, 32, false, 0.8, 1.6},   {64, 32, false, 1.0, 3.2},
+                           {32, 64, false, 1.0, 2.0},  {64, 64, false, 1.0, 3.4},   {64, 128, false, 1.5, 3.4},
+                           {128, 128, false, 2.5, 5.6}, {128, 128, true, 2.0, 6.0}, {256, 256, false, 14.0, 15.7}};
 
 int pick_tile(const GemmArgs &g) {
+  if (g.lda > kTileStride || g.ldw > kTileStride) return 0;
   int best = 0;
   double least = 0;
   for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
     const Tile &t = kTiles[i];
     const int64_t tiles = cdiv(g.n, t.bn) * cdiv(g.m, t.bm);
     if (t.many && tiles <= kCus) continue;
-    const double cost = (double)cdiv(tiles, kCus) * (t.fixed * 1e3 + t.per_k * g.k);
+    const double per_k = t.per_k + (i == 0 ? 0.03 * std::min(g.m, 16) : 0.0);
+    const double cost = (double)cdiv(tiles, kCus) * (t.fixed * 1e3 + per_k * g.k);
     if (i == 0 || cost < least) {
       least = cost;
       best = i;
@@ -64,23 +72,18 @@ int pick_tile(const GemmArgs &g) {
 
 template <typename E>
 void launch(const GemmArgs &g, hipStream_t st) {
-  // Up to 16 tokens each channel's weights go straight to registers: one token
-  // at 4096 x 4096 5.6 us (32 x 32 tiles: 7.6), at 8192 x 28672 40 (45), 16 tokens
-  // at 4096 x 4096 6.5 (7.9); but 16 tokens over 32000 channels 35 (31): there the
-  // tokens, read again by every 16 channels, cost as much as the weights.
-  if (g.m <= 4 || (g.m <= 16 && g.n <= 16384) || g.lda > kTileStride || g.ldw > kTileStride) {
-    hipLaunchKernelGGL((gemm_w8a8_rows_kernel<E, 8>), dim3((unsigned)cdiv(g.n, 16), (unsigned)cdiv(g.m, 16)), dim3(512), 0,
-                       st, g);
-    return;
-  }
   switch (pick_tile(g)) {
-    case 0: launch_tile<E, 32, 32, 1, 1, 4, 256, 4, 2>(g, st); break;
-    case 1: launch_tile<E, 32, 64, 1, 2, 2, 256, 4, 4>(g, st); break;
-    case 2: launch_tile<E, 64, 64, 2, 2, 1, 128, 4, 4>(g, st); break;
-    case 3: launch_tile<E, 64, 64, 2, 2, 1, 128, 2, 4>(g, st); break;
-    case 4: launch_tile<E, 64, 128, 2, 4, 1, 128, 4, 4>(g, st); break;
-    case 5: launch_tile<E, 128, 128, 2, 4, 1, 128, 4, 2>(g, st); break;
-    case 6: launch_tile<E, 128, 128, 2, 4, 1, 128, 2, 2>(g, st); break;
+    case 0:
+      hipLaunchKernelGGL((gemm_w8a8_rows_kernel<E, 8>), dim3((unsigned)cdiv(g.n, 16), (unsigned)cdiv(g.m, 16)), dim3(512), 0,
+                         st, g);
+      break;
+    case 1: launch_tile<E, 32, 32, 1, 1, 4, 256, 4, 2>(g, st); break;
+    case 2: launch_tile<E, 64, 32, 2, 1, 2, 256, 3, 4>(g, st); break;
+    case 3: launch_tile<E, 32, 64, 1, 2, 2, 256, 4, 4>(g, st); break;
+    case 4: launch_tile<E, 64, 64, 2, 2, 1, 128, 4, 4>(g, st); break;
+    case 5: launch_tile<E, 64, 128, 2, 4, 1, 128, 4, 4>(g, st); break;
+    case 6: launch_tile<E, 128, 128, 2, 4, 1, 128, 4, 2>(g, st); break;
+    case 7: launch_tile<E, 128, 128, 2, 4, 1, 128, 2, 2>(g, st); break;
     default: launch_tile<E, 256, 256, 2, 4, 1, 128, 2, 1>(g, st); break;
   }
 }

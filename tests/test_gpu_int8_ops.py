@@ -252,13 +252,21 @@ def test_gemm_w8a8_types(fb, dt, m, n, k):
     gemm_case(fb, m, n, k, dt, bias=True)
 
 
-# (tokens, channels) of which each picks another tile: 32 x 64, 64 x 64, 64 x 128, 128 x 128, 256 x 256
+# (tokens, channels) that take different tiles, some by k
 @pytest.mark.parametrize("m,n", [(61, 8190), (61, 16390), (333, 4093), (1030, 2050), (3500, 4499)])
 @pytest.mark.parametrize("k", [1, 16, 127, 128, 129, 256, 300, 513, 650])
 def test_gemm_w8a8_tiles(fb, m, n, k):
     """Fewer stages than a tile holds, as many, and more, each with and without a tail of k."""
     note(f"gemm_w8a8 tile {m} x {n} x {k}")
     gemm_case(fb, m, n, k, "bf16" if k % 2 else "f16", bias=k > 200, ldy_pad=k % 2)
+
+
+@pytest.mark.parametrize("m,n,k", [(m, n, k) for m, n in ((20, 16384), (7, 30001), (300, 3000)) for k in (1, 127, 256, 257, 511, 700, 1300)]
+                         + [(61, 8190, 1300), (333, 4093, 1100), (3500, 4499, 1000), (3500, 4499, 1024), (3500, 4499, 1153)])
+def test_gemm_w8a8_more_tiles(fb, m, n, k):
+    """64 x 32 and 64 x 64 at all numbers of stages; the largest tile, which takes long k, with and without a tail."""
+    note(f"gemm_w8a8 tile {m} x {n} x {k}")
+    gemm_case(fb, m, n, k, "f32" if k % 2 else "bf16", bias=True, pad=16, ldy_pad=k % 3)
 
 
 def test_gemm_w8a8_wide_strides(fb):
