@@ -29,7 +29,7 @@ struct LogprobArgs {
   int64_t *top_index;
   uint8_t *workspace;                    // splits > 1: the partial results
   int64_t rows, ld;
-  int32_t vocab, top_k, splits, split_len;  // split_len: columns per split, a multiple of kStep
+  int32_t vocab, top_k, splits, split_len;  // split_len: columns per split, a multiple of 64
   float scale;
 };
 

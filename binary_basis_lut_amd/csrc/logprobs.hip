@@ -18,16 +18,17 @@ struct LpPlan {
   int32_t splits, split_len;
 };
 
-// Few rows are split until about kTargetGroups workgroups result, a split
-// taking at least one step of kLpStep columns.
+// Few rows are split until about kTargetGroups workgroups result, a split taking
+// at least one step of kLpStep columns; all splits are equally long (but for
+// whole 64 columns), so that none is too short for a close bound of its best.
 LpPlan plan_of(int64_t rows, int64_t vocab) {
   const int64_t steps = cdiv(vocab, kLpStep);
   int64_t splits = rows > 0 ? std::max<int64_t>(1, kTargetGroups / rows) : 1;
   splits = std::min<int64_t>({splits, steps, (int64_t)kMaxSplitsPerRow});
   const int64_t per = cdiv(steps, splits);
   LpPlan p;
-  p.splits = (int32_t)cdiv(steps, per);
-  p.split_len = (int32_t)(per * kLpStep);
+  p.split_len = (int32_t)(cdiv(cdiv(vocab, cdiv(steps, per)), 64) * 64);
+  p.splits = (int32_t)cdiv(vocab, p.split_len);
   return p;
 }
 
