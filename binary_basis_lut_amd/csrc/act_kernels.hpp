@@ -189,7 +189,7 @@ __attribute__((amdgpu_waves_per_eu(TPR == 1024 && U <= 2 && sizeof(typename E::r
 
 // Rows beyond the registers of a workgroup, and rows shorter than a unit: two
 // passes over the row, the second one from the caches.
-template <typename E, bool NORM>
+template <typename E, bool NORM, bool TINY>
 __global__ __launch_bounds__(1024) void act_long_rows_kernel(const ActArgs a) {
   typedef typename E::raw raw;
   constexpr int W = 16;
@@ -203,9 +203,12 @@ __global__ __launch_bounds__(1024) void act_long_rows_kernel(const ActArgs a) {
     float ss = 0.0f;
     uint32_t ab = 0;
     for (int64_t at = (int64_t)threadIdx.x * kUnit; at < n; at += 1024 * kUnit) {
-      typename E::unit h = load_part<E, true, int64_t>(x, at, n, 0.0f), rv, wv;
-      if (add) rv = load_part<E, true, int64_t>(res, at, n, 0.0f);
-      if (NORM) wv = load_part<E, true, int64_t>(wt, at, n, 0.0f);
+      typename E::unit h = load_part<E, TINY, int64_t>(x, at, n, 0.0f), rv, wv;
+      if (add) rv = load_part<E, TINY, int64_t>(res, at, n, 0.0f);
+      if (NORM) wv = load_part<E, TINY, int64_t>(wt, at, n, 0.0f);
+      settle_part<E, TINY, int64_t>(h, at, n, 0.0f);
+      if (add) settle_part<E, TINY, int64_t>(rv, at, n, 0.0f);
+      if (NORM) settle_part<E, TINY, int64_t>(wv, at, n, 0.0f);
       take_unit<E, NORM>(h, rv, wv, add, ss, ab);
     }
     if (NORM) ss = wave_reduce<SumF>(ss);
@@ -225,11 +228,14 @@ __global__ __launch_bounds__(1024) void act_long_rows_kernel(const ActArgs a) {
     __syncthreads();
     const RowScale rs = row_scale(ss, ab, NORM, a.inv_cols, a.eps);
     for (int64_t at = (int64_t)threadIdx.x * kUnit; at < n; at += 1024 * kUnit) {
-      // residual_out may be x or residual itself: each thread reads an
-      // element again before it writes that element
-      typename E::unit h = load_part<E, true, int64_t>(x, at, n, 0.0f), rv, wv;
-      if (add) rv = load_part<E, true, int64_t>(res, at, n, 0.0f);
-      if (NORM) wv = load_part<E, true, int64_t>(wt, at, n, 0.0f);
+      // residual_out may be x or residual itself: a thread reads its elements
+      // again before it writes them (of a last unit's others it keeps none)
+      typename E::unit h = load_part<E, TINY, int64_t>(x, at, n, 0.0f), rv, wv;
+      if (add) rv = load_part<E, TINY, int64_t>(res, at, n, 0.0f);
+      if (NORM) wv = load_part<E, TINY, int64_t>(wt, at, n, 0.0f);
+      settle_part<E, TINY, int64_t>(h, at, n, 0.0f);
+      if (add) settle_part<E, TINY, int64_t>(rv, at, n, 0.0f);
+      if (NORM) settle_part<E, TINY, int64_t>(wv, at, n, 0.0f);
       float ss2 = 0.0f;
       uint32_t ab2 = 0;
       take_unit<E, NORM>(h, rv, wv, add, ss2, ab2);

@@ -50,8 +50,9 @@ void launch_rows(const ActArgs &a, hipStream_t st) {
 template <typename E, bool NORM>
 void launch_act(const ActArgs &a, hipStream_t st) {
   const int64_t units = cdiv(a.cols, kUnit);
-  if (a.cols < kUnit || units > 4096)
-    hipLaunchKernelGGL((act_long_rows_kernel<E, NORM>), dim3((unsigned)std::min(a.rows, kMaxGrid)), dim3(1024), 0, st, a);
+  const dim3 rows((unsigned)std::min(a.rows, kMaxGrid));
+  if (a.cols < kUnit) hipLaunchKernelGGL((act_long_rows_kernel<E, NORM, true>), rows, dim3(1024), 0, st, a);
+  else if (units > 4096) hipLaunchKernelGGL((act_long_rows_kernel<E, NORM, false>), rows, dim3(1024), 0, st, a);
   else if (units <= 64) launch_rows<E, NORM, 64, 1>(a, st);
   else if (units <= 128) launch_rows<E, NORM, 64, 2>(a, st);
   else if (units <= 256) launch_rows<E, NORM, 256, 1>(a, st);

@@ -60,6 +60,7 @@ int pick_tile(const GemmArgs &g) {
     const Tile &t = kTiles[i];
     const int64_t tiles = cdiv(g.n, t.bn) * cdiv(g.m, t.bm);
     if (t.many && tiles <= kCus) continue;
+    if (t.bm > 32 && t.bm >= 2 * g.m) continue;  // half empty: a smaller one does the same
     const double per_k = t.per_k + (i == 0 ? 0.03 * std::min(g.m, 16) : 0.0);
     const double cost = (double)cdiv(tiles, kCus) * (t.fixed * 1e3 + per_k * g.k);
     if (i == 0 || cost < least) {

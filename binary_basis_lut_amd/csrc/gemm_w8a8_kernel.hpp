@@ -27,11 +27,21 @@ struct Channels {
 
 __device__ __forceinline__ Channels load_channels(const GemmArgs &g, int n0) {
   Channels c;
+  if (n0 + 4 <= g.n) {
+    const floats4 s = *reinterpret_cast<const floats4 *>(g.w_scale + (uint32_t)n0);
+    const floats4 b = g.bias ? *reinterpret_cast<const floats4 *>(g.bias + (uint32_t)n0) : floats4{0, 0, 0, 0};
 #pragma unroll
-  for (int i = 0; i < 4; ++i) {
-    const int n = min(n0 + i, g.n - 1);
-    c.scale[i] = g.w_scale[n];
-    c.bias[i] = g.bias ? g.bias[n] : 0.0f;
+    for (int i = 0; i < 4; ++i) {
+      c.scale[i] = s[i];
+      c.bias[i] = b[i];
+    }
+  } else {
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const uint32_t n = min(n0 + i, g.n - 1);
+      c.scale[i] = g.w_scale[n];
+      c.bias[i] = g.bias ? g.bias[n] : 0.0f;
+    }
   }
   return c;
 }
@@ -374,48 +384,48 @@ __global__ __launch_bounds__(64 * WN * WM * WK) void gemm_w8a8_tile_kernel(const
         for (int j = 0; j < MT; ++j) acc[i][j] += sums[((v - 1) * WN * WM * NT * MT + pair + i * MT + j) * 64 + lane];
   }
   // Outputs.  A lane holds four channels of one token at a time; stored as they
-  // are, 32 rows would be touched 16 bytes each.  So a wave turns 32 tokens x 32 C
+  // are, 32 rows would be touched 16 bytes each.  So a wave turns its tokens x 32 C
   // channels at a time in a piece of LDS of its own and stores up to 128
   // consecutive bytes of a row.
   typedef typename E::raw raw;
   constexpr int C = NT >= 2 && sizeof(raw) == 2 ? 2 : 1, COLS = 32 * C, PITCH = COLS + 16 / (int)sizeof(raw);
   constexpr int PER = 16 / (int)sizeof(raw), LANES = COLS / PER;  // channels of a 16-byte piece; pieces of a row
-  constexpr int TILES = (WK > 1 ? WN * WM : W);
-  static_assert(NT % C == 0 && sums_bytes + TILES * 32 * PITCH * (int)sizeof(raw) <= S * STAGE, "the turned tiles fit the stages' memory");
+  constexpr int TILES = WN * WM, ROWS = 32 * MT;                  // wave tiles; tokens of one
+  static_assert(NT % C == 0 && sums_bytes + TILES * ROWS * PITCH * (int)sizeof(raw) <= S * STAGE,
+                "the turned tiles fit the stages' memory");
   if (WK == 1) wait_and_meet<0>();  // every wave has read its last fragments
   else __builtin_amdgcn_s_waitcnt(0);
   // (the addresses are not to be computed before the loop and held through it)
-  int ne = n0 + wn * NT * 32, me = m0 + wm * MT * 32;
+  int ne = n0 + wn * NT * 32, me = m0 + wm * ROWS;
   asm volatile("" : "+s"(ne), "+s"(me));
-  raw *out = reinterpret_cast<raw *>(lds + (WK > 1 ? sums_bytes : 0)) + (wn * WM + wm) * 32 * PITCH;
+  raw *out = reinterpret_cast<raw *>(lds + sums_bytes) + (wn * WM + wm) * ROWS * PITCH;
+  float sa[MT];
 #pragma unroll
-  for (int j = 0; j < MT; ++j) {
-    const float sa = g.a_scale[min(me + j * 32 + r, g.m - 1)];
+  for (int j = 0; j < MT; ++j) sa[j] = g.a_scale[(uint32_t)min(me + j * 32 + r, g.m - 1)];
 #pragma unroll
-    for (int i0 = 0; i0 < NT; i0 += C) {
-      // lane l of a 32 x 32 tile holds token l % 32, channels 8 q + 4 (l / 32) .. + 3
+  for (int i0 = 0; i0 < NT; i0 += C) {
+    // lane l of a 32 x 32 tile holds token l % 32, channels 8 q + 4 (l / 32) .. + 3
 #pragma unroll
-      for (int i = i0; i < i0 + C; ++i)
+    for (int i = i0; i < i0 + C; ++i)
 #pragma unroll
-        for (int q = 0; q < 4; ++q) {
-          const Channels c = load_channels(g, ne + i * 32 + 8 * q + 4 * half);
+      for (int q = 0; q < 4; ++q) {
+        const Channels c = load_channels(g, ne + i * 32 + 8 * q + 4 * half);
+#pragma unroll
+        for (int j = 0; j < MT; ++j) {
           raw v[4];
 #pragma unroll
-          for (int e = 0; e < 4; ++e) v[e] = E::round((float)acc[i][j][4 * q + e] * sa * c.scale[e] + c.bias[e]);
-          put4(out + r * PITCH + (i - i0) * 32 + 8 * q + 4 * half, v);
-          if (NT > 2) __builtin_amdgcn_sched_barrier(0);  // (few registers are left beside a large tile's sums)
+          for (int e = 0; e < 4; ++e) v[e] = E::round((float)acc[i][j][4 * q + e] * sa[j] * c.scale[e] + c.bias[e]);
+          put4(out + (j * 32 + r) * PITCH + (i - i0) * 32 + 8 * q + 4 * half, v);
         }
-      __builtin_amdgcn_wave_barrier();
-#pragma unroll
-      for (int p = 0; p < 32 * LANES / 64; ++p) {
-        const int row = (p * 64 + lane) / LANES, col = lane % LANES * PER;
-        const i32x4 v = *reinterpret_cast<const i32x4 *>(out + row * PITCH + col);
-        const int m = me + j * 32 + row, n = ne + i0 * 32 + col;
-        if (m < g.m) store_piece((raw *)g.y + (int64_t)m * g.ldy, n, g.n, v);
       }
-      __builtin_amdgcn_wave_barrier();
-      if (NT > 2) __builtin_amdgcn_sched_barrier(0);
+    __builtin_amdgcn_wave_barrier();
+#pragma unroll
+    for (int p = 0; p < ROWS * LANES / 64; ++p) {
+      const int row = (p * 64 + lane) / LANES, col = lane % LANES * PER;
+      const i32x4 v = *reinterpret_cast<const i32x4 *>(out + row * PITCH + col);
+      if (me + row < g.m) store_piece((raw *)g.y + (int64_t)(me + row) * g.ldy, ne + i0 * 32 + col, g.n, v);
     }
+    __builtin_amdgcn_wave_barrier();
   }
 }
 

@@ -41,7 +41,16 @@ profiles/ (each summary names the exact command).  Two modes:
       tables (fluxbin_probe_lds_lookup_banked) over 2- and 4-chunk regions:
       lookups per second, per CU per clock (2.4 GHz), and the packed-weight
       GB/s that rate would sustain (one lookup per g bits of one row's
-      weights, divided by the batch rows that share them).
+      weights, divided by the batch rows that share them);
+
+  python3 -m binary_basis_lut_amd.profile_workload int8 norm:8192,8192,f16 gemm:333,4096,11008,bf16 score:64,131072,20,bf16
+      the 8-bit operators at given sizes: quant:ROWS,COLS,TYPE (row
+      quantisation), norm:ROWS,COLS,TYPE (residual + RMS norm to int8),
+      gemm:M,N,K,TYPE (int8 product) and score:ROWS,VOCAB,TOP,TYPE (token log
+      probabilities), each on distinct operands that pass the 256 MB Infinity
+      Cache (at most 16 sets of them), as a HIP graph replayed `reps` times:
+      time per call, and the rates of the bytes and operations that the call
+      cannot do without.
 """
 from __future__ import annotations
 
@@ -306,6 +315,71 @@ def run_lookup(args) -> None:
               f"{rate / cus / 2.4e9:.2f} per CU per clock, weight stream it sustains {rate / 1e9:.0f} GB/s", flush=True)
 
 
+def run_int8(args) -> None:
+    import torch
+
+    from binary_basis_lut_amd import fluxbin as F
+
+    types = {"f16": (F.DT_F16, torch.float16), "bf16": (F.DT_BF16, torch.bfloat16), "f32": (F.DT_F32, torch.float32)}
+
+    def randn(rows, cols, dtype):
+        return torch.randn(rows, cols, device="cuda").to(dtype)
+
+    def make(op, sizes, code, dtype):
+        """One set of operands: (call, bytes, operations)."""
+        b = dtype.itemsize
+        if op in ("quant", "norm"):
+            rows, cols = sizes
+            ld = (cols + 15) // 16 * 16
+            x, q = randn(rows, cols, dtype), torch.empty((rows, ld), dtype=torch.int8, device="cuda")
+            scale = torch.empty(rows, device="cuda")
+            if op == "quant":
+                return (lambda: F.fluxbin_quantize_rows(x, cols, code, rows, cols, q, ld, scale)), rows * cols * (b + 1), 0
+            res, out, w = randn(rows, cols, dtype), torch.empty_like(x), randn(1, cols, dtype)[0]
+            return (lambda: F.fluxbin_add_rmsnorm(x, cols, res, cols, w, code, rows, cols, 1e-5, out, cols, None, cols, q, ld,
+                                                  scale)), rows * cols * (3 * b + 1), 0
+        if op == "gemm":
+            m, n, k = sizes
+            ld = (k + 15) // 16 * 16
+            a = (32 * randn(m, ld, torch.float32)).round().clamp(-127, 127).to(torch.int8)
+            w = (32 * randn(n, ld, torch.float32)).round().clamp(-127, 127).to(torch.int8)
+            sa, sw, y = torch.rand(m, device="cuda"), torch.rand(n, device="cuda"), torch.empty((m, n), dtype=dtype, device="cuda")
+            return (lambda: F.fluxbin_gemm_w8a8(a, ld, sa, w, ld, sw, None, m, n, k, y, n, code)), (m + n) * k + m * n * b, 2 * m * n * k
+        rows, vocab, top = sizes
+        x, t = 3 * randn(rows, vocab, dtype), torch.randint(0, vocab, (rows,), device="cuda")
+        lp, ent, tl = (torch.empty(s, device="cuda") for s in ((rows,), (rows,), (rows, top)))
+        ti, ws = torch.empty((rows, top), dtype=torch.int64, device="cuda"), torch.empty(4 << 20, dtype=torch.uint8, device="cuda")
+        return (lambda: F.fluxbin_token_logprobs(x, vocab, code, rows, vocab, 1.0, t, lp, ent, top, tl, ti, ws, 4 << 20)), rows * vocab * b, 0
+
+    for case in args.cases:
+        op, rest = case.split(":")
+        *sizes, kind = rest.split(",")
+        sizes = [int(v) for v in sizes]
+        if op not in ("quant", "norm", "gemm", "score") or kind not in types or len(sizes) != (2 if op in ("quant", "norm") else 3):
+            raise SystemExit(f"unknown case {case}")
+        first = make(op, sizes, *types[kind])
+        calls = [first[0]] + [make(op, sizes, *types[kind])[0] for _ in range(min(15, (512 << 20) // first[1]))]
+        for c in calls[:2]:
+            c()
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for c in calls:
+                c()
+        graph.replay()
+        e0, e1 = torch.cuda.Event(enable_timing=True), torch.cuda.Event(enable_timing=True)
+        e0.record()
+        for _ in range(args.reps):
+            graph.replay()
+        e1.record()
+        torch.cuda.synchronize()
+        s = e0.elapsed_time(e1) * 1e-3 / (args.reps * len(calls))
+        ops = f", {first[2] / s / 1e12:.0f} TOP/s" if first[2] else ""
+        print(f"{case}: {s * 1e6:.2f} us per call ({len(calls)} sets), {first[1] / s / 1e9:.0f} GB/s{ops}", flush=True)
+        del first, calls, graph
+        torch.cuda.empty_cache()
+
+
 def main() -> int:
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     sub = ap.add_subparsers(dest="mode", required=True)
@@ -349,9 +423,12 @@ def main() -> int:
     lk = sub.add_parser("lookup")
     lk.add_argument("--iters", type=int, default=2000)
     lk.add_argument("--reps", type=int, default=5)
+    i8 = sub.add_parser("int8")
+    i8.add_argument("cases", nargs="+", metavar="OP:SIZES,TYPE")
+    i8.add_argument("--reps", type=int, default=5)
     args = ap.parse_args()
     {"gemv": run_gemv, "decompose": run_decompose, "dense": run_dense, "copy": run_copy, "stream": run_stream,
-     "empty": run_empty, "lookup": run_lookup}[args.mode](args)
+     "empty": run_empty, "lookup": run_lookup, "int8": run_int8}[args.mode](args)
     return 0
 
 
