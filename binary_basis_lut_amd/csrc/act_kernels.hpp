@@ -115,9 +115,9 @@ __device__ __forceinline__ void give_unit(const ActArgs &a, int64_t row, I at, c
 // matters is how many bytes of how many rows a CU has in flight, so the row's
 // units stay in registers as they are stored and the instances are chosen for
 // 64 registers or fewer where that is possible.  MI355X: 8192 x 8192 fp16 with a
-// residual (470 MB) 84 us = 5.6 TB/s, 4096 x 4096 24.4 us; fp16 to int8 alone,
-// 8192 x 28672 (705 MB) 145 us = 4.9 TB/s, 30000 x 4000 66 us; one row of 4096
-// 3.5 us against 1.6 us of an empty launch.
+// residual (470 MB) 81 - 85 us = 5.5 - 5.8 TB/s, 4096 x 4096 24.4 us; fp16 to int8
+// alone, 8192 x 28672 (705 MB) 130 - 141 us = 5.0 - 5.4 TB/s, 30000 x 4000 66 us;
+// one row of 4096 3.5 us against 1.6 us of an empty launch.
 //
 // TPR threads per row (64: one wave, several rows to a workgroup), U units of
 // eight elements per thread; the row has at least 8 and at most TPR * U * 8
