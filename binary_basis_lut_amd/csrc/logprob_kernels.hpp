@@ -33,13 +33,16 @@ struct LogprobArgs {
   float scale;
 };
 
-constexpr int kLpThreads = 256;
-constexpr int kLpUnits = 4;                                // units of eight per thread and slice
-constexpr int kLpStep = kLpThreads * kUnit;                // columns of one unit of every thread
-constexpr int kLpSlice = kLpStep * kLpUnits;               // columns held in registers at a time
+// A workgroup of T threads takes a slice of T x kLpUnits units of eight columns at
+// a time: 1024 threads where few rows, each within one slice, have to fill the
+// chip (such a row needs no join of splits), else 256.
+constexpr int kLpFew = 1024, kLpMany = 256;
+constexpr int kLpUnits = 4;                  // units of eight per thread and slice
+constexpr int kLpSmall = kLpMany * kUnit;    // splits up to this length go by single columns
+constexpr int kLpFewCols = kLpFew * kUnit * kLpUnits;  // columns that kLpFew threads hold in registers
 constexpr int kLpMaxTop = 64;
 static_assert(kLpUnits * kUnit == 32, "a thread marks its elements of a slice in one word");
-constexpr int kLpCap = 512;                                // candidate keys that LDS holds
+constexpr int kLpCap = 512;                  // candidate keys that LDS holds
 constexpr float kLn2 = 0.6931471805599453f, kLog2e = 1.4426950408889634f;
 constexpr float kNegInf = -__builtin_inff();
 
@@ -92,20 +95,22 @@ __device__ __forceinline__ Stats join_wave(Stats a, float c) {
 }
 
 // What the waves of a workgroup share while they pick the best keys.
+template <int T>
 struct LpShared {
   uint64_t cand[kLpCap];
   uint64_t list[kLpMaxTop];  // the best keys, in order; 0 past their count
-  Stats wave[kLpThreads / 64];
-  uint64_t wkey[kLpThreads / 64];
-  float wthr[kLpThreads / 64];
+  Stats wave[T / 64];
+  uint64_t wkey[T / 64];
+  float wthr[T / 64];
   int count;
 };
 
 // cand[0, n) -> the best top_k of them in list, in order.
-__device__ __forceinline__ void select_by_rank(LpShared &sh, int n, int top_k) {
+template <int T>
+__device__ __forceinline__ void select_by_rank(LpShared<T> &sh, int n, int top_k) {
   if (threadIdx.x < (unsigned)kLpMaxTop) sh.list[threadIdx.x] = 0;
   __syncthreads();
-  for (int i = threadIdx.x; i < n; i += kLpThreads) {
+  for (int i = threadIdx.x; i < n; i += T) {
     const uint64_t k = sh.cand[i];
     int rank = 0;
 #pragma unroll 8
@@ -115,14 +120,15 @@ __device__ __forceinline__ void select_by_rank(LpShared &sh, int n, int top_k) {
   __syncthreads();
 }
 
-__device__ __forceinline__ uint64_t block_max_key(LpShared &sh, uint64_t k) {
+template <int T>
+__device__ __forceinline__ uint64_t block_max_key(LpShared<T> &sh, uint64_t k) {
   k = wave_reduce<MaxKey>(k);
   __syncthreads();
   if (threadIdx.x % 64 == 0) sh.wkey[threadIdx.x / 64] = k;
   __syncthreads();
   k = sh.wkey[0];
 #pragma unroll
-  for (int i = 1; i < kLpThreads / 64; ++i) k = sh.wkey[i] > k ? sh.wkey[i] : k;
+  for (int i = 1; i < T / 64; ++i) k = sh.wkey[i] > k ? sh.wkey[i] : k;
   return k;
 }
 
@@ -144,14 +150,14 @@ __device__ __forceinline__ float wave_nth(float v, int n) {
   return m;
 }
 
-__device__ __forceinline__ Stats join_block(LpShared &sh, Stats st, float c) {
+// The joined statistics of a workgroup, in every thread.
+template <int T>
+__device__ __forceinline__ Stats join_block(LpShared<T> &sh, Stats st, float c) {
   st = join_wave(st, c);
   if (threadIdx.x % 64 == 0) sh.wave[threadIdx.x / 64] = st;
   __syncthreads();
-  st = sh.wave[0];
-#pragma unroll
-  for (int i = 1; i < kLpThreads / 64; ++i) st = join(st, sh.wave[i], c);
-  return st;
+  const unsigned lane = threadIdx.x % 64;
+  return join_wave(lane < T / 64 ? sh.wave[lane] : Stats{kNegInf, 0.0f, 0.0f}, c);
 }
 
 // A row's target and its logit, fetched by thread 0 ahead of their use (first
@@ -208,19 +214,20 @@ __host__ __device__ inline int64_t lp_part_bytes(int top_k) { return 16 + 8 * (i
 // that defeat this (long runs of equal logits, ascending rows, fewer than top_k
 // logits left unmasked) are taken again, one key at a time.
 //
-// SMALL (splits of at most kLpStep columns): a thread takes single columns, 256
+// SMALL (splits of at most kLpSmall columns): a thread takes single columns, T
 // apart, instead of eight in a row, so that all threads have their part of a
 // short row and its bound is close.
 //
 // Bound by the HBM read for fp32 rows (4096 x 32000, 524 MB, in 92 us = 5.7 TB/s);
 // for 16-bit rows the exponential, a quarter-rate instruction, and the
 // conversions weigh as much (about 11 issue slots per element; 4096 x 32000
-// fp16 in 68 us = 3.9 TB/s).  Few rows are latency: 6 us, and 4 for the join.
-template <typename E, bool SMALL>
-__global__ __launch_bounds__(kLpThreads) void logprob_rows_kernel(const LogprobArgs a) {
+// fp16 in 68 us = 3.9 TB/s).  Few rows are latency: 6 us per kernel at 2000 to
+// 5000 columns, 9 at 32000, or 6 and 4 more for the join where a row is split.
+template <typename E, bool SMALL, int T>
+__global__ __launch_bounds__(T) void logprob_rows_kernel(const LogprobArgs a) {
   typedef typename E::raw raw;
-  constexpr int kWaves = kLpThreads / 64, U = SMALL ? 1 : kLpUnits;
-  __shared__ LpShared sh;
+  constexpr int kWaves = T / 64, U = SMALL ? 1 : kLpUnits, kStep = T * kUnit, kSlice = kStep * U;
+  __shared__ LpShared<T> sh;
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x / a.splits;
   const int split = (int)(blockIdx.x % a.splits);
@@ -233,23 +240,23 @@ __global__ __launch_bounds__(kLpThreads) void logprob_rows_kernel(const LogprobA
   bool full = false;  // more candidates than LDS holds
   if (tid == 0) sh.count = 0;
   Target target = a.splits == 1 ? target_index(a, row) : Target{-1, 0.0f};
-  for (int at0 = begin; at0 < end; at0 += kLpSlice, ++slice) {
+  for (int at0 = begin; at0 < end; at0 += kSlice, ++slice) {
     typename E::unit v[U];
-    const int units = min(U, (end - at0 + kLpStep - 1) / kLpStep);  // units that hold columns
+    const int units = min(U, (end - at0 + kStep - 1) / kStep);  // units that hold columns
     float tm = kNegInf;
     if (SMALL) {
       v[0].fill(E::round(kNegInf));
 #pragma unroll
       for (int i = 0; i < kUnit; ++i)
-        if (at0 + i * kLpThreads + tid < end) v[0].put(i, x[at0 + i * kLpThreads + tid]);
+        if (at0 + i * T + tid < end) v[0].put(i, x[at0 + i * T + tid]);
     } else {
 #pragma unroll
-      for (int u = 0; u < U; ++u) v[u] = load_part<E, false, int>(x, at0 + (u * kLpThreads + tid) * kUnit, end, kNegInf);
+      for (int u = 0; u < U; ++u) v[u] = load_part<E, false, int>(x, at0 + (u * T + tid) * kUnit, end, kNegInf);
     }
 #pragma unroll
     for (int u = 0; u < U; ++u) {
       if (u >= units) break;
-      if (!SMALL) settle_part<E, false, int>(v[u], at0 + (u * kLpThreads + tid) * kUnit, end, kNegInf);
+      if (!SMALL) settle_part<E, false, int>(v[u], at0 + (u * T + tid) * kUnit, end, kNegInf);
 #pragma unroll
       for (int i = 0; i < kUnit; ++i) tm = fmaxf(tm, v[u].get(i));
     }
@@ -288,14 +295,14 @@ __global__ __launch_bounds__(kLpThreads) void logprob_rows_kernel(const LogprobA
       int p = atomicAdd(&sh.count, (int)__builtin_popcount(mask));
       while (mask) {  // few
         const int j = __builtin_clz(mask) - (32 - kUnit * U);
-        const int at = at0 + (SMALL ? j * kLpThreads + tid : ((j / kUnit) * kLpThreads + tid) * kUnit + j % kUnit);
+        const int at = at0 + (SMALL ? j * T + tid : ((j / kUnit) * T + tid) * kUnit + j % kUnit);
         mask &= ~(1u << (kUnit * U - 1 - j));
         if (p < kLpCap) sh.cand[p] = key_of(E::unit::pick(v, j), at);
         ++p;
       }
     }
     if (slice == 0) least = above(thr);
-    if (slice > 0 && (slice & (slice + 1)) == 0 && at0 + kLpSlice < end && !full) {
+    if (slice > 0 && (slice & (slice + 1)) == 0 && at0 + kSlice < end && !full) {
       __syncthreads();
       const int n = sh.count;
       full = n > kLpCap;
@@ -319,7 +326,7 @@ __global__ __launch_bounds__(kLpThreads) void logprob_rows_kernel(const LogprobA
       uint64_t below = ~0ull;
       for (int j = 0; j < a.top_k; ++j) {
         uint64_t best = 0;
-        for (int at = begin + tid; at < end; at += kLpThreads) {
+        for (int at = begin + tid; at < end; at += T) {
           const float f = E::load(x[at]);
           const uint64_t k = key_of(f, at);
           if (f == f && k < below && k > best) best = k;
@@ -344,10 +351,10 @@ __global__ __launch_bounds__(kLpThreads) void logprob_rows_kernel(const LogprobA
   }
 }
 
-// Joins the splits of a row (at most kLpThreads of them).
+// Joins the splits of a row (at most kLpMany of them).
 template <typename E>
-__global__ __launch_bounds__(kLpThreads) void logprob_join_kernel(const LogprobArgs a) {
-  __shared__ LpShared sh;
+__global__ __launch_bounds__(kLpMany) void logprob_join_kernel(const LogprobArgs a) {
+  __shared__ LpShared<kLpMany> sh;
   const int tid = threadIdx.x;
   const int64_t row = blockIdx.x, pb = lp_part_bytes(a.top_k);
   const uint8_t *base = a.workspace + row * a.splits * pb;
@@ -375,7 +382,7 @@ __global__ __launch_bounds__(kLpThreads) void logprob_join_kernel(const LogprobA
     if (tid < a.splits && rank == (a.top_k + t - 1) / t - 1) sh.wkey[0] = mine;
     __syncthreads();
     const uint64_t bound = sh.wkey[0];
-    for (int i = tid; i < a.splits * a.top_k; i += kLpThreads) {
+    for (int i = tid; i < a.splits * a.top_k; i += kLpMany) {
       const uint64_t k = ((const uint64_t *)(base + (i / a.top_k) * pb + 16))[i % a.top_k];
       if (k >= bound && k > 0) {
         const int p = atomicAdd(&sh.count, 1);

@@ -10,23 +10,32 @@ using namespace fluxbin;
 namespace {
 
 constexpr int64_t kTargetGroups = 1024;
+constexpr int64_t kFewRows = 256;  // one per CU
 constexpr int64_t kMaxRows = (int64_t)1 << 22;
 constexpr int64_t kMaxVocab = (int64_t)1 << 28;
-constexpr int kMaxSplitsPerRow = 128;
+constexpr int64_t kMaxSplitsPerRow = 128;
 
 struct LpPlan {
-  int32_t splits, split_len;
+  int32_t threads, splits, split_len;
 };
 
-// Few rows are split until about kTargetGroups workgroups result, a split taking
-// at least one step of kLpStep columns; all splits are equally long (but for
-// whole 64 columns), so that none is too short for a close bound of its best.
+// Up to kFewRows rows that kLpFew threads hold in registers get one workgroup
+// each and need no join: against splits and a join 1 x 5000 fp16 takes 6.3 us
+// for 8.5, 1 x 32000 9.3 for 9.2, 64 x 32000 fp32 10.5 for 12.0, 256 x 32000
+// 13.4 for 17.4; with two such workgroups on a CU the gain ends (400 x 32000
+// fp32 25.7 for 24.4, 512 x 8000 18.0 for 15.6).
+// Other rows are split, where they are few, until about kTargetGroups workgroups
+// of kLpMany threads result (64 x 131072 by one workgroup of kLpFew threads per
+// row takes 26.2 us, by splits 17.3), a split taking at least one step of
+// kLpSmall columns; all splits are equally long (but for whole 64 columns), so
+// that none is too short for a close bound of its best.
 LpPlan plan_of(int64_t rows, int64_t vocab) {
-  const int64_t steps = cdiv(vocab, kLpStep);
+  if (rows <= kFewRows && vocab > kLpSmall && vocab <= kLpFewCols) return LpPlan{kLpFew, 1, (int32_t)(cdiv(vocab, 64) * 64)};
+  const int64_t steps = cdiv(vocab, kLpSmall);
   int64_t splits = rows > 0 ? std::max<int64_t>(1, kTargetGroups / rows) : 1;
-  splits = std::min<int64_t>({splits, steps, (int64_t)kMaxSplitsPerRow});
+  splits = std::min<int64_t>({splits, steps, kMaxSplitsPerRow});
   const int64_t per = cdiv(steps, splits);
-  LpPlan p;
+  LpPlan p{kLpMany, 1, 0};
   p.split_len = (int32_t)(cdiv(cdiv(vocab, cdiv(steps, per)), 64) * 64);
   p.splits = (int32_t)cdiv(vocab, p.split_len);
   return p;
@@ -47,11 +56,12 @@ size_t ws_bytes(int64_t rows, const LpPlan &p, int32_t top_k) {
 }
 
 template <typename E>
-void launch(const LogprobArgs &a, hipStream_t st) {
-  const dim3 grid((unsigned)(a.rows * a.splits)), block(kLpThreads);
-  if (a.split_len <= kLpStep) hipLaunchKernelGGL((logprob_rows_kernel<E, true>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((logprob_rows_kernel<E, false>), grid, block, 0, st, a);
-  if (a.splits > 1) hipLaunchKernelGGL(logprob_join_kernel<E>, dim3((unsigned)a.rows), dim3(kLpThreads), 0, st, a);
+void launch(const LogprobArgs &a, int threads, hipStream_t st) {
+  const dim3 grid((unsigned)(a.rows * a.splits)), block(threads);
+  if (threads == kLpFew) hipLaunchKernelGGL((logprob_rows_kernel<E, false, kLpFew>), grid, block, 0, st, a);
+  else if (a.split_len <= kLpSmall) hipLaunchKernelGGL((logprob_rows_kernel<E, true, kLpMany>), grid, block, 0, st, a);
+  else hipLaunchKernelGGL((logprob_rows_kernel<E, false, kLpMany>), grid, block, 0, st, a);
+  if (a.splits > 1) hipLaunchKernelGGL(logprob_join_kernel<E>, dim3((unsigned)a.rows), dim3(kLpMany), 0, st, a);
 }
 
 }  // namespace
@@ -106,9 +116,9 @@ fluxbin_status fluxbin_token_logprobs(const void *logits, int64_t ld, int32_t dt
   a.split_len = p.split_len;
   a.scale = logit_scale;
   hipStream_t s = (hipStream_t)stream;
-  if (dtype == FLUXBIN_DT_F16) launch<F16>(a, s);
-  else if (dtype == FLUXBIN_DT_BF16) launch<BF16>(a, s);
-  else launch<F32>(a, s);
+  if (dtype == FLUXBIN_DT_F16) launch<F16>(a, p.threads, s);
+  else if (dtype == FLUXBIN_DT_BF16) launch<BF16>(a, p.threads, s);
+  else launch<F32>(a, p.threads, s);
   const hipError_t e = hipGetLastError();
   return e != hipSuccess ? hip_fail(e, "token logprobs launch") : ok();
 }

@@ -94,8 +94,8 @@ def score_args(**kw):
     (dict(targets=None), 1), (dict(logprob=None), 1), (dict(targets=None, logprob=None, entropy=None, top_k=0), 1),
     (dict(logits=None), 1), (dict(top_index=None), 1), (dict(top_logprob=None), 1), (dict(ld=31999), 1),
     (dict(logits=A + 1), 1), (dict(targets=A + 4), 1), (dict(logprob=A + 2), 1), (dict(entropy=A + 2), 1),
-    (dict(top_index=A + 4), 1), (dict(top_logprob=A + 2), 1), (dict(workspace=None), 3), (dict(workspace_bytes=8), 3),
-    (dict(workspace=A + 8), 1),
+    (dict(top_index=A + 4), 1), (dict(top_logprob=A + 2), 1), (dict(vocab=300000, ld=300000, workspace=None), 3),
+    (dict(vocab=300000, ld=300000, workspace_bytes=8), 3), (dict(vocab=300000, ld=300000, workspace=A + 8), 1),
 ])
 def test_token_logprobs_refuses(fb, kw, status):
     refused(fb, "fluxbin_token_logprobs", score_args(**kw), status)
