@@ -45,25 +45,27 @@ void launch_tile(const GemmArgs &g, hipStream_t st) {
 //   8192 x 28672 x 8192     -     -    -     -     -     -   2480        -    1740
 struct Tile {
   int bn, bm;
+  int threads;
   bool many;            // for more tiles than CUs only
   double fixed, per_k;  // us, ns
 };
-constexpr Tile kTiles[] = {{16, 16, false, 0.3, 0.6},  {32, 32, false, 0.8, 1.6},   {64, 32, false, 1.0, 3.2},
-                           {32, 64, false, 1.0, 2.0},  {64, 64, false, 1.0, 3.4},   {64, 128, false, 1.5, 3.4},
-                           {128, 128, false, 2.5, 5.6}, {128, 128, true, 2.0, 6.0}, {256, 256, false, 14.0, 15.7}};
+constexpr Tile kTiles[] = {{16, 16, 512, false, 0.3, 0.6},   {32, 32, 256, false, 0.8, 1.6},  {64, 32, 256, false, 1.0, 3.2},
+                           {32, 64, 256, false, 1.0, 2.0},   {64, 64, 256, false, 1.0, 3.4},  {64, 128, 512, false, 1.5, 3.4},
+                           {128, 128, 512, false, 2.5, 5.6}, {128, 128, 512, true, 2.0, 6.0}, {256, 256, 512, false, 14.0, 15.7}};
 
 int pick_tile(const GemmArgs &g) {
   if (g.lda > kTileStride || g.ldw > kTileStride) return 0;
   int best = 0;
-  double least = 0;
+  double least = __builtin_inf();
   for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
     const Tile &t = kTiles[i];
     const int64_t tiles = cdiv(g.n, t.bn) * cdiv(g.m, t.bm);
     if (t.many && tiles <= kCus) continue;
+    if (tiles * t.threads >= (int64_t)1 << 32) continue;  // a grid has fewer threads than that
     if (t.bm > 32 && t.bm >= 2 * g.m) continue;  // half empty: a smaller one does the same
     const double per_k = t.per_k + (i == 0 ? 0.03 * std::min(g.m, 16) : 0.0);
     const double cost = (double)cdiv(tiles, kCus) * (t.fixed * 1e3 + per_k * g.k);
-    if (i == 0 || cost < least) {
+    if (cost < least) {
       least = cost;
       best = i;
     }

@@ -284,6 +284,25 @@ def test_gemm_w8a8_wide_strides(fb):
     assert torch.equal(y.cpu().double(), a.double() @ w.double().t())  # below 2^24: exact in fp32
 
 
+def test_gemm_w8a8_most_channels(fb):
+    """2^27 channels: tiles of 16 channels by 512 threads would make a grid of 2^32 threads."""
+    m, n, k = 1, 1 << 27, 304
+    note(f"gemm_w8a8 {m} x {n} x {k}")
+    if torch.cuda.mem_get_info()[0] < 60 << 30:
+        pytest.skip("needs 42 GB of GPU memory")
+    w = torch.zeros((n, k), dtype=torch.int8, device="cuda")
+    at = torch.tensor([0, 1 << 26, n - 17, n - 1], device="cuda")
+    w[at, 300] = torch.tensor([1, -2, 3, 127], dtype=torch.int8, device="cuda")
+    a = torch.full((m, k), 2, dtype=torch.int8, device="cuda")
+    one = torch.ones(n, device="cuda")
+    y = torch.full((m, n), 9.0, device="cuda")
+    fb.fluxbin_gemm_w8a8(a, k, one, w, k, one, None, m, n, k, y, n, fb.DT_F32)
+    torch.cuda.synchronize()
+    assert y[0, at].tolist() == [2.0, -4.0, 6.0, 254.0]
+    y[0, at] = 0
+    assert not y.any()
+
+
 def test_outputs_beyond_32_bit_offsets(fb):
     note("gemm_w8a8, quantize_rows and token_logprobs over more than 2^31 elements")
     m, n, k = 40000, 60000, 64
