@@ -35,10 +35,12 @@ struct LogprobArgs {
 
 // A workgroup of T threads takes a slice of T x kLpUnits units of eight columns at
 // a time: 1024 threads where few rows, each within one slice, have to fill the
-// chip (such a row needs no join of splits), else 256.
-constexpr int kLpFew = 1024, kLpMany = 256;
+// chip (such a row needs no join of splits), else 256; rows of a few hundred
+// columns go to one wave each.
+constexpr int kLpFew = 1024, kLpMany = 256, kLpTiny = 64;
 constexpr int kLpUnits = 4;                  // units of eight per thread and slice
 constexpr int kLpSmall = kLpMany * kUnit;    // splits up to this length go by single columns
+constexpr int kLpTinyCols = kLpTiny * kUnit;  // rows up to this length, by single columns too
 constexpr int kLpFewCols = kLpFew * kUnit * kLpUnits;  // columns that kLpFew threads hold in registers
 constexpr int kLpMaxTop = 64;
 static_assert(kLpUnits * kUnit == 32, "a thread marks its elements of a slice in one word");
@@ -156,6 +158,7 @@ __device__ __forceinline__ Stats join_block(LpShared<T> &sh, Stats st, float c) 
   st = join_wave(st, c);
   if (threadIdx.x % 64 == 0) sh.wave[threadIdx.x / 64] = st;
   __syncthreads();
+  if (T == 64) return st;
   const unsigned lane = threadIdx.x % 64;
   return join_wave(lane < T / 64 ? sh.wave[lane] : Stats{kNegInf, 0.0f, 0.0f}, c);
 }

@@ -11,6 +11,7 @@ namespace {
 
 constexpr int64_t kTargetGroups = 1024;
 constexpr int64_t kFewRows = 256;  // one per CU
+constexpr int32_t kTinyTop = 32;
 constexpr int64_t kMaxRows = (int64_t)1 << 22;
 constexpr int64_t kMaxVocab = (int64_t)1 << 28;
 constexpr int64_t kMaxSplitsPerRow = 128;
@@ -29,8 +30,15 @@ struct LpPlan {
 // row takes 26.2 us, by splits 17.3), a split taking at least one step of
 // kLpSmall columns; all splits are equally long (but for whole 64 columns), so
 // that none is too short for a close bound of its best.
-LpPlan plan_of(int64_t rows, int64_t vocab) {
+// Rows of at most kLpTinyCols columns go to one wave each, without barriers to
+// wait at: 12837 x 257 fp16 9.8 us for 26.0 with 256 threads, with 20 best 20.5
+// for 53.5, 32 best 22.9 for 55.3; 73 x 320, 20 best, 6.0 for 6.5; one row about
+// the same. More alternatives than kTinyTop leave the bound, the least of 64
+// maxima, too low (12837 x 500 with 64 best: 120 us, 256 threads 68; 73 x 320
+// with 40 best 8.1, 256 threads 7.4).
+LpPlan plan_of(int64_t rows, int64_t vocab, int32_t top_k) {
   if (rows <= kFewRows && vocab > kLpSmall && vocab <= kLpFewCols) return LpPlan{kLpFew, 1, (int32_t)(cdiv(vocab, 64) * 64)};
+  if (vocab <= kLpTinyCols && top_k <= kTinyTop) return LpPlan{kLpTiny, 1, (int32_t)(cdiv(vocab, 64) * 64)};
   const int64_t steps = cdiv(vocab, kLpSmall);
   int64_t splits = rows > 0 ? std::max<int64_t>(1, kTargetGroups / rows) : 1;
   splits = std::min<int64_t>({splits, steps, kMaxSplitsPerRow});
@@ -59,6 +67,7 @@ template <typename E>
 void launch(const LogprobArgs &a, int threads, hipStream_t st) {
   const dim3 grid((unsigned)(a.rows * a.splits)), block(threads);
   if (threads == kLpFew) hipLaunchKernelGGL((logprob_rows_kernel<E, false, kLpFew>), grid, block, 0, st, a);
+  else if (threads == kLpTiny) hipLaunchKernelGGL((logprob_rows_kernel<E, true, kLpTiny>), grid, block, 0, st, a);
   else if (a.split_len <= kLpSmall) hipLaunchKernelGGL((logprob_rows_kernel<E, true, kLpMany>), grid, block, 0, st, a);
   else hipLaunchKernelGGL((logprob_rows_kernel<E, false, kLpMany>), grid, block, 0, st, a);
   if (a.splits > 1) hipLaunchKernelGGL(logprob_join_kernel<E>, dim3((unsigned)a.rows), dim3(kLpMany), 0, st, a);
@@ -72,7 +81,7 @@ fluxbin_status fluxbin_token_logprobs_workspace_size(int64_t rows, int64_t vocab
   const fluxbin_status st = check_shape(rows, vocab, top_k);
   if (st) return st;
   if (!bytes) return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "bytes is NULL");
-  *bytes = ws_bytes(rows, plan_of(rows, vocab), top_k);
+  *bytes = ws_bytes(rows, plan_of(rows, vocab, top_k), top_k);
   return ok();
 }
 
@@ -95,7 +104,7 @@ fluxbin_status fluxbin_token_logprobs(const void *logits, int64_t ld, int32_t dt
   if (!aligned(logits, dtype == FLUXBIN_DT_F32 ? 4 : 2) || !aligned(targets, 8) || !aligned(logprob, 4) ||
       !aligned(entropy, 4) || (top_k && (!aligned(top_logprob, 4) || !aligned(top_index, 8))))
     return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "a pointer is not aligned to its elements");
-  const LpPlan p = plan_of(rows, vocab);
+  const LpPlan p = plan_of(rows, vocab, top_k);
   const size_t need = ws_bytes(rows, p, top_k);
   if (need && (!workspace || workspace_bytes < need))
     return fail(FLUXBIN_ERR_WORKSPACE, "workspace of %zu bytes needed, %zu given", need, workspace ? workspace_bytes : (size_t)0);

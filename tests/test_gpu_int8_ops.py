@@ -436,7 +436,8 @@ def test_token_logprobs_many_rows(fb, dt, rows, vocab, top_k):
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16", "f32"])
-@pytest.mark.parametrize("rows,vocab,top_k", [(9, 2050, 64), (2, 32760, 20), (40, 32768, 5), (2, 32769, 64), (256, 2100, 5), (257, 2100, 5)])
+@pytest.mark.parametrize("rows,vocab,top_k", [(9, 2050, 64), (2, 32760, 20), (40, 32768, 5), (2, 32769, 64), (256, 2100, 5), (257, 2100, 5),
+                                              (7, 512, 32), (7, 512, 33), (7, 513, 32), (3000, 257, 20), (3000, 60, 32)])
 def test_token_logprobs_around_the_plans_borders(fb, dt, rows, vocab, top_k):
     note(f"token_logprobs {dt} {rows} x {vocab} top {top_k}")
     g = torch.Generator().manual_seed(vocab)
@@ -445,12 +446,12 @@ def test_token_logprobs_around_the_plans_borders(fb, dt, rows, vocab, top_k):
     check_scores(x, score(fb, x, dt, top_k, 1.0, targets, ld=vocab + 3, offset=1), 1.0, top_k, targets)
 
 
-@pytest.mark.parametrize("rows", [1, 2, 1500])
-@pytest.mark.parametrize("top_k", [1, 5, 64])
+@pytest.mark.parametrize("rows", [1, 2, 5, 1500])
+@pytest.mark.parametrize("top_k", [1, 5, 30, 64])
 @pytest.mark.parametrize("pattern", ["equal", "two values", "ascending", "descending", "few left", "none left", "zeros of both signs",
                                      "lowest value", "lowest throughout", "peaked", "huge"])
 def test_token_logprobs_hard_rows(fb, rows, top_k, pattern):
-    vocab = {1: 17000, 2: 40000}.get(rows, 9000)
+    vocab = {1: 17000, 2: 40000, 5: 500}.get(rows, 9000)
     note(f"token_logprobs {pattern} {rows} x {vocab} top {top_k}")
     g = torch.Generator().manual_seed(5)
     x = torch.randn(rows, vocab, generator=g)
@@ -475,7 +476,7 @@ def test_token_logprobs_hard_rows(fb, rows, top_k, pattern):
     elif pattern == "lowest throughout":
         x[:] = torch.finfo(torch.float32).min
     elif pattern == "peaked":
-        x[:, 4321] = 200.0
+        x[:, min(4321, vocab // 2)] = 200.0
     elif pattern == "huge":
         x = x * 3000
     targets = torch.full((rows,), 8 if pattern == "lowest value" else 7, dtype=torch.int64)
