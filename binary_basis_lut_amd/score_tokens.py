@@ -21,13 +21,20 @@ from __future__ import annotations
 import argparse
 
 
+def _check(name, t, dtype, device, shape) -> None:
+    """Raises ValueError unless `t` is what the kernels, which see its address only, will take it for."""
+    if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape):
+        raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, not {dtype} {tuple(shape)} on {device}")
+
+
 class ScoringHead:
     """Final norm, int8 output head and scoring for up to `max_rows` rows at a time.
 
     norm_weight: fp16 [hidden]; head: fp16 [vocab][hidden] (quantised here, per
     output channel; the tensor is not kept).  score() enqueues three calls on
-    the current stream and returns views of buffers that the next call
-    overwrites; it allocates nothing, so it can be captured in a graph.
+    the current stream, and a copy of the targets where they are not adjacent,
+    and returns views of buffers that the next call overwrites; it allocates
+    nothing, so it can be captured in a graph.
     """
 
     def __init__(self, norm_weight, head, max_rows: int, top_k: int = 5, eps: float = 1e-5):
@@ -38,7 +45,7 @@ class ScoringHead:
         self.vocab, self.hidden = head.shape
         if norm_weight.dtype != torch.float16 or head.dtype != torch.float16:
             raise ValueError("norm_weight and head must be fp16")
-        dev = head.device
+        dev = self.device = head.device
         self.norm_weight = norm_weight.contiguous()
         self.ld = (self.hidden + 15) // 16 * 16  # the int8 product wants rows of whole 16-byte pieces
         empty = lambda *shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device=dev)
@@ -47,17 +54,23 @@ class ScoringHead:
         self.residual = empty(max_rows, self.hidden, dtype=torch.float16)
         self.q, self.scale = empty(max_rows, self.ld, dtype=torch.int8), empty(max_rows)
         self.logits = empty(max_rows, self.vocab)
+        self.targets = empty(max_rows, dtype=torch.int64)
         self.logprob, self.entropy = empty(max_rows), empty(max_rows)
         self.top_logprob, self.top_index = empty(max_rows, top_k), empty(max_rows, top_k, dtype=torch.int64)
         need = max(F.fluxbin_token_logprobs_workspace_size(r, self.vocab, top_k) for r in range(1, max_rows + 1))
         self.workspace = empty(max(need, 16), dtype=torch.uint8)
 
     def score(self, y, residual, targets, logit_scale: float = 1.0) -> dict:
-        """y, residual: fp16 [rows][hidden]; targets: int64 [rows], negative where there is none."""
+        """y, residual: fp16 [rows][hidden]; targets: int64 [rows], any stride, negative where there is none."""
+        import torch
+
         F, rows = self.F, y.shape[0]
         if rows > self.logits.shape[0] or y.shape[1] != self.hidden or residual.shape != y.shape:
             raise ValueError(f"y {tuple(y.shape)}, residual {tuple(residual.shape)}: at most {self.logits.shape[0]} rows "
                              f"of {self.hidden}")
+        _check("targets", targets, torch.int64, self.device, (rows,))
+        if not targets.is_contiguous():  # one step's column of a [rows][steps] matrix
+            targets = self.targets[:rows].copy_(targets)
         F.fluxbin_add_rmsnorm(y, y.stride(0), residual, residual.stride(0), self.norm_weight, F.DT_F16, rows, self.hidden,
                               self.eps, self.residual, self.hidden, None, 0, self.q, self.ld, self.scale)
         F.fluxbin_gemm_w8a8(self.q, self.ld, self.scale, self.head_q, self.ld, self.head_scale, None, rows, self.vocab,

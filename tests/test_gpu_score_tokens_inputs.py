@@ -1,0 +1,56 @@
+"""ScoringHead on inputs that do not lie in memory as its buffers do."""
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+HIDDEN, VOCAB = 512, 3000
+
+
+def make(rows):
+    from binary_basis_lut_amd.score_tokens import ScoringHead
+    g = torch.Generator().manual_seed(rows)
+    norm = (1 + 0.1 * torch.randn(HIDDEN, generator=g)).half().cuda()
+    head = (torch.randn(VOCAB, HIDDEN, generator=g) * 0.05).half().cuda()
+    y, residual = torch.randn(rows, HIDDEN, generator=g).half().cuda(), torch.randn(rows, HIDDEN, generator=g).half().cuda()
+    return ScoringHead(norm, head, rows), y, residual, g
+
+
+def kept(out):
+    torch.cuda.synchronize()
+    return {n: v.clone() for n, v in out.items()}
+
+
+def same(a, b):
+    for n in a:
+        assert torch.equal(a[n], b[n]), n
+
+
+@pytest.mark.parametrize("rows", [1, 4, 33])
+def test_a_step_of_a_token_matrix_scores_its_own_tokens(rows):
+    print(f"[case] score, {rows} strided targets", flush=True)
+    head, y, residual, g = make(rows)
+    tokens = torch.randint(0, VOCAB, (rows, 7), generator=g).cuda()
+    for t in range(7):
+        want = kept(head.score(y, residual, tokens[:, t].contiguous()))
+        same(kept(head.score(y, residual, tokens[:, t])), want)
+    lp = torch.log_softmax(want["logits"].double(), 1)
+    assert torch.allclose(want["logprob"].double(), lp.gather(1, tokens[:, 6:])[:, 0], rtol=0, atol=1e-4)
+
+
+def test_strided_targets_are_read_anew_by_every_replay():
+    rows = 5
+    print("[case] score, strided targets in a graph", flush=True)
+    head, y, residual, g = make(rows)
+    tokens = torch.randint(0, VOCAB, (rows, 4), generator=g).cuda()
+    head.score(y, residual, tokens[:, 1])
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        out = head.score(y, residual, tokens[:, 1])
+    for _ in range(3):
+        tokens.copy_(torch.randint(0, VOCAB, (rows, 4), generator=g))
+        graph.replay()
+        got = kept(out)
+        same(kept(head.score(y, residual, tokens[:, 1].contiguous())), got)

@@ -1,0 +1,80 @@
+"""What ScoringHead refuses and what it hands to the kernels, without a GPU.
+
+The tensors are fake ones that say they are on cuda:0 and hold nothing, and the launching entry points
+are replaced by recorders, so a call that is let through is seen by its arguments.
+"""
+import pytest
+
+torch = pytest.importorskip("torch")
+
+HIDDEN, VOCAB, ROWS = 512, 1000, 3
+
+
+@pytest.fixture
+def calls(monkeypatch):
+    from torch._subclasses.fake_tensor import FakeTensorMode
+
+    from binary_basis_lut_amd import build as B
+    if B.is_stale():
+        B.build()
+    from binary_basis_lut_amd import fluxbin
+
+    class Stream:
+        cuda_stream = 0
+
+        def synchronize(self):
+            seen.append(("synchronize",))
+
+    seen = []
+    for name in ("fluxbin_quantize_rows", "fluxbin_add_rmsnorm", "fluxbin_gemm_w8a8", "fluxbin_token_logprobs"):
+        monkeypatch.setattr(fluxbin, name, lambda *a, _n=name: seen.append((_n, *a)))
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 0)
+    monkeypatch.setattr(torch.cuda, "current_stream", lambda device=None: Stream())
+    with FakeTensorMode():
+        yield seen
+
+
+def fp16(*shape, device="cuda"):
+    return torch.empty(shape, dtype=torch.float16, device=device)
+
+
+def int64(*shape, device="cuda"):
+    return torch.empty(shape, dtype=torch.int64, device=device)
+
+
+def make(rows=8):
+    from binary_basis_lut_amd.score_tokens import ScoringHead
+    return ScoringHead(fp16(HIDDEN), fp16(VOCAB, HIDDEN), rows)
+
+
+def scored(calls, head, y, residual, targets):
+    calls.clear()
+    head.score(y, residual, targets)
+    return {c[0]: c[1:] for c in calls}
+
+
+def refused(calls, head, y, residual, targets, name):
+    calls.clear()
+    with pytest.raises(ValueError, match=name):
+        head.score(y, residual, targets)
+    assert not calls  # before any launch
+
+
+@pytest.mark.parametrize("targets", [
+    lambda: int64(ROWS).to(torch.int32), lambda: int64(ROWS - 1), lambda: int64(ROWS + 1), lambda: int64(0),
+    lambda: int64(ROWS, 1), lambda: int64(ROWS, device="cpu"), lambda: fp16(ROWS),
+], ids=["int32", "too few", "too many", "none", "2-D", "host memory", "fp16"])
+def test_targets_that_would_be_misread_are_refused(calls, targets):
+    refused(calls, make(), fp16(ROWS, HIDDEN), fp16(ROWS, HIDDEN), targets(), "targets")
+
+
+@pytest.mark.parametrize("rows", [1, 2, ROWS, 8])
+def test_targets_of_one_step_of_a_token_matrix_arrive_one_behind_the_other(calls, rows):
+    tokens = int64(rows, 17)
+    given = scored(calls, make(), fp16(rows, HIDDEN), fp16(rows, HIDDEN), tokens[:, 5])["fluxbin_token_logprobs"][6]
+    assert given.dtype == torch.int64 and given.shape == (rows,) and given.is_contiguous()
+
+
+def test_adjacent_targets_are_passed_as_they_are(calls):
+    targets = int64(9)[4:4 + ROWS]
+    assert scored(calls, make(), fp16(ROWS, HIDDEN), fp16(ROWS, HIDDEN), targets)["fluxbin_token_logprobs"][6] is targets
