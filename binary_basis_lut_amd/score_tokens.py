@@ -25,6 +25,8 @@ def _check(name, t, dtype, device, shape) -> None:
     """Raises ValueError unless `t` is what the kernels, which see its address only, will take it for."""
     if t.dtype != dtype or t.device != device or tuple(t.shape) != tuple(shape):
         raise ValueError(f"{name}: {t.dtype} {tuple(t.shape)} on {t.device}, not {dtype} {tuple(shape)} on {device}")
+    if t.dim() == 2 and t.shape[1] > 1 and t.stride(1) != 1:
+        raise ValueError(f"{name}: the elements of a row lie {t.stride(1)} apart, not side by side")
 
 
 class ScoringHead:
@@ -61,13 +63,14 @@ class ScoringHead:
         self.workspace = empty(max(need, 16), dtype=torch.uint8)
 
     def score(self, y, residual, targets, logit_scale: float = 1.0) -> dict:
-        """y, residual: fp16 [rows][hidden]; targets: int64 [rows], any stride, negative where there is none."""
+        """y, residual: fp16 [rows][hidden], any row stride; targets: int64 [rows], any stride, negative where there is none."""
         import torch
 
         F, rows = self.F, y.shape[0]
-        if rows > self.logits.shape[0] or y.shape[1] != self.hidden or residual.shape != y.shape:
-            raise ValueError(f"y {tuple(y.shape)}, residual {tuple(residual.shape)}: at most {self.logits.shape[0]} rows "
-                             f"of {self.hidden}")
+        if rows > self.logits.shape[0]:
+            raise ValueError(f"y {tuple(y.shape)}: at most {self.logits.shape[0]} rows of {self.hidden}")
+        _check("y", y, torch.float16, self.device, (rows, self.hidden))
+        _check("residual", residual, torch.float16, self.device, (rows, self.hidden))
         _check("targets", targets, torch.int64, self.device, (rows,))
         if not targets.is_contiguous():  # one step's column of a [rows][steps] matrix
             targets = self.targets[:rows].copy_(targets)

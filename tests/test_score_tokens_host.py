@@ -78,3 +78,23 @@ def test_targets_of_one_step_of_a_token_matrix_arrive_one_behind_the_other(calls
 def test_adjacent_targets_are_passed_as_they_are(calls):
     targets = int64(9)[4:4 + ROWS]
     assert scored(calls, make(), fp16(ROWS, HIDDEN), fp16(ROWS, HIDDEN), targets)["fluxbin_token_logprobs"][6] is targets
+
+
+@pytest.mark.parametrize("bad", [
+    lambda: fp16(ROWS, HIDDEN).to(torch.bfloat16), lambda: fp16(ROWS, HIDDEN).float(), lambda: fp16(ROWS, 2 * HIDDEN)[:, ::2],
+    lambda: fp16(HIDDEN, ROWS).t(), lambda: fp16(ROWS, HIDDEN, device="cpu"),
+], ids=["bf16", "fp32", "every other column", "transposed", "host memory"])
+@pytest.mark.parametrize("which", ["y", "residual"])
+def test_activations_that_would_be_misread_are_refused(calls, which, bad):
+    t = {"y": fp16(ROWS, HIDDEN), "residual": fp16(ROWS, HIDDEN), which: bad()}
+    refused(calls, make(), t["y"], t["residual"], int64(ROWS), which)
+
+
+@pytest.mark.parametrize("shape", [(HIDDEN,), (ROWS, HIDDEN, 1), (0, HIDDEN + 1)])
+def test_activations_of_another_shape_are_refused(calls, shape):
+    refused(calls, make(), fp16(*shape), fp16(*shape), int64(ROWS), "y")
+
+
+def test_activations_whose_rows_lie_apart_go_with_their_stride(calls):
+    norm = scored(calls, make(), fp16(ROWS, 2 * HIDDEN)[:, :HIDDEN], fp16(2 * ROWS, HIDDEN)[::2], int64(ROWS))["fluxbin_add_rmsnorm"]
+    assert norm[1] == 2 * HIDDEN and norm[3] == 2 * HIDDEN
