@@ -29,6 +29,10 @@ def _check(name, t, dtype, device, shape) -> None:
         raise ValueError(f"{name}: the elements of a row lie {t.stride(1)} apart, not side by side")
 
 
+def _row_stride(t) -> int:
+    return t.stride(0) if t.shape[0] > 1 else t.shape[1]  # a single row's stride can be any number
+
+
 class ScoringHead:
     """Final norm, int8 output head and scoring for up to `max_rows` rows at a time.
 
@@ -52,7 +56,7 @@ class ScoringHead:
         self.ld = (self.hidden + 15) // 16 * 16  # the int8 product wants rows of whole 16-byte pieces
         empty = lambda *shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device=dev)
         self.head_q, self.head_scale = empty(self.vocab, self.ld, dtype=torch.int8), empty(self.vocab)
-        F.fluxbin_quantize_rows(head, head.stride(0), F.DT_F16, self.vocab, self.hidden, self.head_q, self.ld, self.head_scale)
+        F.fluxbin_quantize_rows(head, _row_stride(head), F.DT_F16, self.vocab, self.hidden, self.head_q, self.ld, self.head_scale)
         self.residual = empty(max_rows, self.hidden, dtype=torch.float16)
         self.q, self.scale = empty(max_rows, self.ld, dtype=torch.int8), empty(max_rows)
         self.logits = empty(max_rows, self.vocab)
@@ -74,7 +78,7 @@ class ScoringHead:
         _check("targets", targets, torch.int64, self.device, (rows,))
         if not targets.is_contiguous():  # one step's column of a [rows][steps] matrix
             targets = self.targets[:rows].copy_(targets)
-        F.fluxbin_add_rmsnorm(y, y.stride(0), residual, residual.stride(0), self.norm_weight, F.DT_F16, rows, self.hidden,
+        F.fluxbin_add_rmsnorm(y, _row_stride(y), residual, _row_stride(residual), self.norm_weight, F.DT_F16, rows, self.hidden,
                               self.eps, self.residual, self.hidden, None, 0, self.q, self.ld, self.scale)
         F.fluxbin_gemm_w8a8(self.q, self.ld, self.scale, self.head_q, self.ld, self.head_scale, None, rows, self.vocab,
                             self.hidden, self.logits, self.vocab, F.DT_F32)

@@ -98,3 +98,10 @@ def test_activations_of_another_shape_are_refused(calls, shape):
 def test_activations_whose_rows_lie_apart_go_with_their_stride(calls):
     norm = scored(calls, make(), fp16(ROWS, 2 * HIDDEN)[:, :HIDDEN], fp16(2 * ROWS, HIDDEN)[::2], int64(ROWS))["fluxbin_add_rmsnorm"]
     assert norm[1] == 2 * HIDDEN and norm[3] == 2 * HIDDEN
+
+
+def test_a_single_row_is_scored_whatever_its_row_stride_says(calls):
+    row = fp16(HIDDEN, 1).t()  # adjacent elements; a stride between rows that are not there
+    assert row.is_contiguous() and row.stride(0) < HIDDEN
+    norm = scored(calls, make(), row, row, int64(1))["fluxbin_add_rmsnorm"]
+    assert norm[1] >= HIDDEN and norm[3] >= HIDDEN  # below that fluxbin_add_rmsnorm refuses the call
