@@ -48,10 +48,12 @@ class ScoringHead:
         from . import fluxbin as F
 
         self.F, self.top_k, self.eps = F, top_k, eps
+        if head.dim() != 2 or not head.is_cuda:
+            raise ValueError(f"head: {tuple(head.shape)} on {head.device}, not [vocab][hidden] on a GPU")
         self.vocab, self.hidden = head.shape
-        if norm_weight.dtype != torch.float16 or head.dtype != torch.float16:
-            raise ValueError("norm_weight and head must be fp16")
         dev = self.device = head.device
+        _check("head", head, torch.float16, dev, head.shape)
+        _check("norm_weight", norm_weight, torch.float16, dev, (self.hidden,))
         self.norm_weight = norm_weight.contiguous()
         self.ld = (self.hidden + 15) // 16 * 16  # the int8 product wants rows of whole 16-byte pieces
         empty = lambda *shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device=dev)

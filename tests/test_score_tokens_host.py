@@ -105,3 +105,26 @@ def test_a_single_row_is_scored_whatever_its_row_stride_says(calls):
     assert row.is_contiguous() and row.stride(0) < HIDDEN
     norm = scored(calls, make(), row, row, int64(1))["fluxbin_add_rmsnorm"]
     assert norm[1] >= HIDDEN and norm[3] >= HIDDEN  # below that fluxbin_add_rmsnorm refuses the call
+
+
+@pytest.mark.parametrize("norm,head,name", [
+    (lambda: fp16(HIDDEN - 1), lambda: fp16(VOCAB, HIDDEN), "norm_weight"), (lambda: fp16(HIDDEN + 1), lambda: fp16(VOCAB, HIDDEN), "norm_weight"),
+    (lambda: fp16(1, HIDDEN), lambda: fp16(VOCAB, HIDDEN), "norm_weight"),
+    (lambda: fp16(HIDDEN, device="cpu"), lambda: fp16(VOCAB, HIDDEN), "norm_weight"),
+    (lambda: fp16(HIDDEN).to(torch.bfloat16), lambda: fp16(VOCAB, HIDDEN), "norm_weight"),
+    (lambda: fp16(HIDDEN), lambda: fp16(HIDDEN, VOCAB).t(), "head"), (lambda: fp16(HIDDEN), lambda: fp16(VOCAB, 2 * HIDDEN)[:, ::2], "head"),
+    (lambda: fp16(HIDDEN), lambda: fp16(VOCAB, HIDDEN).float(), "head"), (lambda: fp16(HIDDEN), lambda: fp16(VOCAB * HIDDEN), "head"),
+    (lambda: fp16(HIDDEN, device="cpu"), lambda: fp16(VOCAB, HIDDEN, device="cpu"), "head"),
+], ids=["short norm", "long norm", "2-D norm", "norm in host memory", "bf16 norm", "transposed head", "every other column", "fp32 head",
+        "flat head", "host memory"])
+def test_weights_that_would_be_misread_are_refused(calls, norm, head, name):
+    from binary_basis_lut_amd.score_tokens import ScoringHead
+    with pytest.raises(ValueError, match=name):
+        ScoringHead(norm(), head(), 4)
+    assert not calls
+
+
+def test_weights_with_strides_are_taken(calls):
+    from binary_basis_lut_amd.score_tokens import ScoringHead
+    h = ScoringHead(fp16(2 * HIDDEN)[::2], fp16(VOCAB, HIDDEN + 8)[:, :HIDDEN], 4)
+    assert h.norm_weight.is_contiguous() and calls[0][:3] == ("fluxbin_quantize_rows", calls[0][1], HIDDEN + 8)
