@@ -37,10 +37,13 @@ class ScoringHead:
     """Final norm, int8 output head and scoring for up to `max_rows` rows at a time.
 
     norm_weight: fp16 [hidden]; head: fp16 [vocab][hidden] (quantised here, per
-    output channel; the tensor is not kept).  score() enqueues three calls on
+    output channel; the tensor is not kept; the constructor waits for it, so
+    that score() may run on any stream).  score() enqueues three calls on
     the current stream, and a copy of the targets where they are not adjacent,
     and returns views of buffers that the next call overwrites; it allocates
-    nothing, so it can be captured in a graph.
+    nothing, so it can be captured in a graph.  Calls of one head share these
+    buffers: the caller orders calls on different streams, and of the inputs
+    only `residual` may be one of the views (the last call's, all its rows).
     """
 
     def __init__(self, norm_weight, head, max_rows: int, top_k: int = 5, eps: float = 1e-5):
@@ -67,6 +70,7 @@ class ScoringHead:
         self.top_logprob, self.top_index = empty(max_rows, top_k), empty(max_rows, top_k, dtype=torch.int64)
         need = max(F.fluxbin_token_logprobs_workspace_size(r, self.vocab, top_k) for r in range(1, max_rows + 1))
         self.workspace = empty(max(need, 16), dtype=torch.uint8)
+        torch.cuda.current_stream().synchronize()  # the quantised head is there for a score() on any stream
 
     def score(self, y, residual, targets, logit_scale: float = 1.0) -> dict:
         """y, residual: fp16 [rows][hidden], any row stride; targets: int64 [rows], any stride, negative where there is none."""

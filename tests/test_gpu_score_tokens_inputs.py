@@ -69,3 +69,27 @@ def test_rows_that_lie_apart_score_as_adjacent_ones():
     wide, twice = torch.zeros(rows, HIDDEN + 9, dtype=y.dtype, device="cuda"), torch.zeros(2 * rows, HIDDEN, dtype=y.dtype, device="cuda")
     wide[:, 3:3 + HIDDEN], twice[::2] = y, residual
     same(kept(head.score(wide[:, 3:3 + HIDDEN], twice[::2], targets)), want)
+
+
+def test_a_head_made_on_one_stream_scores_on_another():
+    rows = 4
+    print("[case] score on another stream than the constructor's", flush=True)
+    head, y, residual, g = make(rows)
+    targets = torch.randint(0, VOCAB, (rows,), generator=g).cuda()
+    want = kept(head.score(y, residual, targets))
+    side = torch.cuda.Stream()
+    side.wait_stream(torch.cuda.current_stream())
+    with torch.cuda.stream(side):
+        other = make(rows)[0]
+    same(kept(other.score(y, residual, targets)), want)
+
+
+def test_the_last_residual_is_taken_in_place():
+    rows = 5
+    print("[case] score with the residual view of the call before", flush=True)
+    head, y, residual, g = make(rows)
+    targets = torch.randint(0, VOCAB, (rows,), generator=g).cuda()
+    between = kept(head.score(y, residual, targets))["residual"]
+    want = kept(head.score(y, between, targets))
+    out = head.score(y, residual, targets)
+    same(kept(head.score(y, out["residual"], targets)), want)

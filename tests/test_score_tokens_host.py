@@ -128,3 +128,15 @@ def test_weights_with_strides_are_taken(calls):
     from binary_basis_lut_amd.score_tokens import ScoringHead
     h = ScoringHead(fp16(2 * HIDDEN)[::2], fp16(VOCAB, HIDDEN + 8)[:, :HIDDEN], 4)
     assert h.norm_weight.is_contiguous() and calls[0][:3] == ("fluxbin_quantize_rows", calls[0][1], HIDDEN + 8)
+
+
+def test_the_quantised_head_is_finished_before_a_score_on_any_stream(calls):
+    make()
+    names = [c[0] for c in calls]
+    assert names == ["fluxbin_quantize_rows", "synchronize"]
+
+
+def test_a_score_waits_for_nothing(calls):
+    head = make()
+    scored(calls, head, fp16(ROWS, HIDDEN), fp16(ROWS, HIDDEN), int64(ROWS, 2)[:, 0])
+    assert ("synchronize",) not in calls
