@@ -29,6 +29,13 @@ def _check(name, t, dtype, device, shape) -> None:
         raise ValueError(f"{name}: the elements of a row lie {t.stride(1)} apart, not side by side")
 
 
+def _check_current(device) -> None:
+    import torch
+
+    if torch.cuda.current_device() != device.index:  # where the launches go
+        raise ValueError(f"the head is on {device}, the current device is cuda:{torch.cuda.current_device()}")
+
+
 def _row_stride(t) -> int:
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]  # a single row's stride can be any number
 
@@ -57,6 +64,7 @@ class ScoringHead:
         dev = self.device = head.device
         _check("head", head, torch.float16, dev, head.shape)
         _check("norm_weight", norm_weight, torch.float16, dev, (self.hidden,))
+        _check_current(dev)
         self.norm_weight = norm_weight.contiguous()
         self.ld = (self.hidden + 15) // 16 * 16  # the int8 product wants rows of whole 16-byte pieces
         empty = lambda *shape, dtype=torch.float32: torch.empty(shape, dtype=dtype, device=dev)
@@ -82,6 +90,7 @@ class ScoringHead:
         _check("y", y, torch.float16, self.device, (rows, self.hidden))
         _check("residual", residual, torch.float16, self.device, (rows, self.hidden))
         _check("targets", targets, torch.int64, self.device, (rows,))
+        _check_current(self.device)
         if not targets.is_contiguous():  # one step's column of a [rows][steps] matrix
             targets = self.targets[:rows].copy_(targets)
         F.fluxbin_add_rmsnorm(y, _row_stride(y), residual, _row_stride(residual), self.norm_weight, F.DT_F16, rows, self.hidden,

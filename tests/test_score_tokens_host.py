@@ -140,3 +140,14 @@ def test_a_score_waits_for_nothing(calls):
     head = make()
     scored(calls, head, fp16(ROWS, HIDDEN), fp16(ROWS, HIDDEN), int64(ROWS, 2)[:, 0])
     assert ("synchronize",) not in calls
+
+
+def test_another_current_device_is_refused(calls, monkeypatch):
+    """The launches go to the current device, which need not reach another one's memory."""
+    from binary_basis_lut_amd.score_tokens import ScoringHead
+    head = make()
+    monkeypatch.setattr(torch.cuda, "current_device", lambda: 1)
+    refused(calls, head, fp16(ROWS, HIDDEN), fp16(ROWS, HIDDEN), int64(ROWS), "cuda:1")
+    with pytest.raises(ValueError, match="cuda:1"):
+        ScoringHead(fp16(HIDDEN, device="cuda:0"), fp16(VOCAB, HIDDEN, device="cuda:0"), 4)
+    assert not calls
