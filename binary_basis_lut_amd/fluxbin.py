@@ -132,6 +132,7 @@ def _ptr(a):
     return a.data_ptr()
 
 
+_device = None      # () -> torch's current device, set before the next
 _raw_stream = None  # (device) -> handle of torch's current stream, once torch runs on a GPU
 
 
@@ -143,7 +144,8 @@ def _stream(stream):
             return _raw_stream(_device())
         import torch
         if torch.cuda.is_initialized():
-            _raw_stream, _device = torch._C._cuda_getCurrentRawStream, torch._C._cuda_getDevice
+            _device = torch._C._cuda_getDevice
+            _raw_stream = torch._C._cuda_getCurrentRawStream  # last: other threads go by it
         return torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
