@@ -12,6 +12,7 @@ There is no CPU fallback.
 from __future__ import annotations
 
 import ctypes
+import os
 from pathlib import Path
 
 LIB_PATH = Path(__file__).resolve().parent / "_build" / "libfluxbin.so"
@@ -134,6 +135,14 @@ def _ptr(a):
 
 _device = None      # () -> torch's current device, set before the next
 _raw_stream = None  # (device) -> handle of torch's current stream, once torch runs on a GPU
+
+
+def _forget_stream():
+    global _raw_stream
+    _raw_stream = None  # a forked child has no GPU: torch says so when it is asked again
+
+
+os.register_at_fork(after_in_child=_forget_stream)
 
 
 def _stream(stream):

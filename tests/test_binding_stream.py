@@ -1,4 +1,5 @@
 """The binding's look-up of torch's current stream, on the host: a stand-in for the GPU's part of torch."""
+import os
 import sys
 import threading
 
@@ -76,3 +77,25 @@ def test_a_thread_that_looks_between_any_two_steps_gets_a_stream(fb):
     finally:
         sys.settrace(before)
     assert len(first) > 10 and not wrong, wrong
+
+
+def test_a_forked_child_is_refused_as_torch_refuses_it(fb, monkeypatch):
+    """The parent's streams mean nothing in a child: there torch itself has to answer again."""
+    assert fb._stream(None) == 5 and fb._raw_stream is not None
+
+    def refuse(device=None):
+        raise RuntimeError("Cannot re-initialize CUDA in forked subprocess")
+
+    pid = os.fork()
+    if pid == 0:
+        status = 1
+        try:
+            torch.cuda.is_initialized, torch.cuda.current_stream = lambda: False, refuse  # as torch does in a child
+            try:
+                fb._stream(None)
+            except RuntimeError:
+                status = 0
+        finally:
+            os._exit(status)
+    assert os.waitstatus_to_exitcode(os.waitpid(pid, 0)[1]) == 0
+    assert fb._raw_stream is not None and fb._stream(None) == 5  # the parent goes on as before
