@@ -13,11 +13,34 @@ constexpr int64_t kMaxK = 131071;            // 131071 * 128 * 128 < 2^31
 constexpr int64_t kCus = 256;                // compute units of an MI355X
 constexpr int64_t kMaxMN = (int64_t)1 << 27;
 constexpr int64_t kTileStride = (int64_t)1 << 23;  // 256 strides stay below 2^31 (32-bit offsets)
+constexpr int64_t kRowsN = (int64_t)1 << 26;       // channels and tokens of one launch of the kernel without
+constexpr int64_t kRowsM = (int64_t)1 << 19;       // tiles: 2^31 threads along x, 2^15 workgroups along y
 
 template <typename E, int BN, int BM, int WN, int WM, int WK, int KB, int S, int G>
 void launch_tile(const GemmArgs &g, hipStream_t st) {
   hipLaunchKernelGGL((gemm_w8a8_tile_kernel<E, BN, BM, WN, WM, WK, KB, S, G>),
                      dim3((unsigned)(cdiv(g.n, BN) * cdiv(g.m, BM))), dim3(64 * WN * WM * WK), 0, st, g);
+}
+
+// The kernel without tiles has a workgroup for 16 channels (x) and 16 tokens (y);
+// sizes beyond a grid (fewer than 2^32 threads along x, at most 65535 workgroups
+// along y) take several launches.  Only strides that rule the tiles out come to that.
+template <typename E>
+void launch_rows(const GemmArgs &g, hipStream_t st) {
+  for (int64_t m0 = 0; m0 < g.m; m0 += kRowsM)
+    for (int64_t n0 = 0; n0 < g.n; n0 += kRowsN) {
+      GemmArgs part = g;
+      part.a += m0 * g.lda;
+      part.a_scale += m0;
+      part.w += n0 * g.ldw;
+      part.w_scale += n0;
+      if (g.bias) part.bias += n0;
+      part.y = (typename E::raw *)g.y + m0 * g.ldy + n0;
+      part.m = (int32_t)std::min(g.m - m0, kRowsM);
+      part.n = (int32_t)std::min(g.n - n0, kRowsN);
+      hipLaunchKernelGGL((gemm_w8a8_rows_kernel<E, 8>), dim3((unsigned)cdiv(part.n, 16), (unsigned)cdiv(part.m, 16)), dim3(512),
+                         0, st, part);
+    }
 }
 
 // Which kernel and tile (channels x tokens): a CU takes ceil(tiles / 256) of them,
@@ -54,7 +77,8 @@ constexpr Tile kTiles[] = {{16, 16, 512, false, 0.3, 0.6},   {32, 32, 256, false
                            {128, 128, 512, false, 2.5, 5.6}, {128, 128, 512, true, 2.0, 6.0}, {256, 256, 512, false, 14.0, 15.7}};
 
 int pick_tile(const GemmArgs &g) {
-  if (g.lda > kTileStride || g.ldw > kTileStride) return 0;
+  // (the stride of a single row leads nowhere)
+  if ((g.m > 1 && g.lda > kTileStride) || (g.n > 1 && g.ldw > kTileStride)) return 0;
   int best = 0;
   double least = __builtin_inf();
   for (int i = 0; i < (int)(sizeof(kTiles) / sizeof(kTiles[0])); ++i) {
@@ -76,10 +100,7 @@ int pick_tile(const GemmArgs &g) {
 template <typename E>
 void launch(const GemmArgs &g, hipStream_t st) {
   switch (pick_tile(g)) {
-    case 0:
-      hipLaunchKernelGGL((gemm_w8a8_rows_kernel<E, 8>), dim3((unsigned)cdiv(g.n, 16), (unsigned)cdiv(g.m, 16)), dim3(512), 0,
-                         st, g);
-      break;
+    case 0: launch_rows<E>(g, st); break;
     case 1: launch_tile<E, 32, 32, 1, 1, 4, 256, 4, 2>(g, st); break;
     case 2: launch_tile<E, 64, 32, 2, 1, 2, 256, 3, 4>(g, st); break;
     case 3: launch_tile<E, 32, 64, 1, 2, 2, 256, 4, 4>(g, st); break;
