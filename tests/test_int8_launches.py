@@ -1,6 +1,8 @@
 """The launches of the 8-bit operators, watched on the host (tests/launches.py)."""
+import numpy as np
 import pytest
 
+from tests import int8_cases as C
 from tests import launches as L
 
 pytestmark = pytest.mark.skipif(not L.available(), reason="gcc and c++filt not available")
@@ -79,3 +81,64 @@ def test_products_of_all_sizes_fit_their_grids():
     for call, launches in zip(calls, recorded(calls)):
         check_gemm(call, launches)
         assert len(launches) == 1
+
+
+def instances(kernels, prefix):
+    return {k for k in kernels if k.startswith(prefix)}
+
+
+@pytest.fixture(scope="module")
+def kernels():
+    return L.record([])[0]
+
+
+def test_the_table_of_tiles_reaches_every_instance_of_the_product(kernels):
+    calls, want = [], []
+    for tile, (params, (m, n), _, _) in C.TILES.items():
+        for dt in C.TYPES:
+            for k in C.tile_ks(tile):
+                calls.append(L.gemm(m, n, k, dt))
+                want.append(f"gemm_w8a8_{'rows' if tile == '16x16' else 'tile'}_kernel<{dt.upper()}, {params}>")
+    got = recorded(calls)
+    for call, launches, name in zip(calls, got, want):
+        assert [x["kernel"] for x in launches] == [name], call
+        check_gemm(call, launches)
+    assert set(want) == instances(kernels, "gemm_w8a8_")
+
+
+def test_the_table_of_plans_reaches_every_instance_of_the_scores(kernels):
+    seen = set()
+    for plan, (rows, vocab, params, splits, slices) in C.PLANS.items():
+        calls = [L.score(rows, vocab, k, dt) for dt in C.TYPES for k in C.plan_top_ks(plan)]
+        for call, launches in zip(calls, recorded(calls)):
+            dt = {v: k for k, v in L.TYPES.items()}[call[1][2]].upper()
+            names = [f"logprob_rows_kernel<{dt}, {params}>"] + [f"logprob_join_kernel<{dt}>"] * (splits > 1)
+            assert [x["kernel"] for x in launches] == names, (plan, call)
+            a, threads = launches[0]["args"], int(params.split(", ")[1])
+            assert a["splits"] == splits and launches[0]["grid"] == [rows * splits, 1, 1], (plan, a)
+            assert cdiv(min(a["split_len"], vocab), threads * 8 * (1 if "true" in params else 4)) == slices, (plan, a)
+            assert splits * a["split_len"] >= vocab > (splits - 1) * a["split_len"]
+            for x in launches:
+                check_grid(x)
+            seen.update(names)
+    assert seen == instances(kernels, "logprob_")
+
+
+@pytest.mark.parametrize("dt", C.TYPES)
+def test_the_products_comparison_sees_what_is_wrong(dt):
+    want = np.array([1.0, -2.0, 0.0, 70000.0, -70000.0, 1000.0])
+    mag = np.abs(want)
+    right = want.copy()
+    if dt == "f16":
+        right[3:5] = np.inf, -np.inf
+    assert not C.product_errors(right, want, mag, dt).any()
+    for i in range(len(want)):
+        for wrong in (np.nan, -right[i] if right[i] else 1e-3, 3.0, np.inf if right[i] != np.inf else 65504.0):
+            got = right.copy()
+            got[i] = wrong
+            assert C.product_errors(got, want, mag, dt).tolist() == [j == i for j in range(len(want))], (i, wrong)
+    # the border of fp16's largest number and infinity
+    border = np.array([65519.0, 65521.0])
+    if dt == "f16":
+        assert not C.product_errors(np.array([65504.0, np.inf]), border, border, dt).any()
+        assert C.product_errors(np.array([np.inf, 65504.0]), border, np.zeros(2), dt).all()
