@@ -46,6 +46,8 @@ profiles/ (each summary names the exact command).  Two modes:
   python3 -m binary_basis_lut_amd.profile_workload int8 norm:8192,8192,f16 gemm:333,4096,11008,bf16 score:64,131072,20,bf16
       the 8-bit operators at given sizes: quant:ROWS,COLS,TYPE (row
       quantisation), norm:ROWS,COLS,TYPE (residual + RMS norm to int8),
+      keep:ROWS,COLS,TYPE (the same kept in the activation type, as the
+      binary-basis layers take it), rms:ROWS,COLS,TYPE (that without a residual),
       gemm:M,N,K,TYPE (int8 product) and score:ROWS,VOCAB,TOP,TYPE (token log
       probabilities), each on distinct operands that pass the 256 MB Infinity
       Cache (at most 16 sets of them), as a HIP graph replayed `reps` times:
@@ -328,14 +330,23 @@ def run_int8(args) -> None:
     def make(op, sizes, code, dtype):
         """One set of operands: (call, bytes, operations)."""
         b = dtype.itemsize
-        if op in ("quant", "norm"):
+        if op in ("quant", "norm", "keep", "rms"):
             rows, cols = sizes
             ld = (cols + 15) // 16 * 16
             x, q = randn(rows, cols, dtype), torch.empty((rows, ld), dtype=torch.int8, device="cuda")
             scale = torch.empty(rows, device="cuda")
             if op == "quant":
                 return (lambda: F.fluxbin_quantize_rows(x, cols, code, rows, cols, q, ld, scale)), rows * cols * (b + 1), 0
-            res, out, w = randn(rows, cols, dtype), torch.empty_like(x), randn(1, cols, dtype)[0]
+            w = randn(1, cols, dtype)[0]
+            if op == "rms":
+                y = torch.empty_like(x)
+                return (lambda: F.fluxbin_add_rmsnorm(x, cols, None, 0, w, code, rows, cols, 1e-5, None, 0, y, cols, None, 0,
+                                                      None)), rows * cols * 2 * b, 0
+            res, out = randn(rows, cols, dtype), torch.empty_like(x)
+            if op == "keep":
+                y = torch.empty_like(x)
+                return (lambda: F.fluxbin_add_rmsnorm(x, cols, res, cols, w, code, rows, cols, 1e-5, out, cols, y, cols, None, 0,
+                                                      None)), rows * cols * 4 * b, 0
             return (lambda: F.fluxbin_add_rmsnorm(x, cols, res, cols, w, code, rows, cols, 1e-5, out, cols, None, cols, q, ld,
                                                   scale)), rows * cols * (3 * b + 1), 0
         if op == "gemm":
@@ -355,7 +366,8 @@ def run_int8(args) -> None:
         op, rest = case.split(":")
         *sizes, kind = rest.split(",")
         sizes = [int(v) for v in sizes]
-        if op not in ("quant", "norm", "gemm", "score") or kind not in types or len(sizes) != (2 if op in ("quant", "norm") else 3):
+        ops = {"quant": 2, "norm": 2, "keep": 2, "rms": 2, "gemm": 3, "score": 3}
+        if kind not in types or ops.get(op) != len(sizes):
             raise SystemExit(f"unknown case {case}")
         first = make(op, sizes, *types[kind])
         calls = [first[0]] + [make(op, sizes, *types[kind])[0] for _ in range(min(15, (512 << 20) // first[1]))]
