@@ -113,11 +113,15 @@ __device__ __forceinline__ void give_unit(const ActArgs &a, int64_t row, I at, c
 
 // Memory-bound: a row is read once and its results written once, and what
 // matters is how many bytes of how many rows a CU has in flight, so the row's
-// units stay in registers as they are stored and the instances are chosen for
-// 64 registers or fewer where that is possible.  MI355X: 8192 x 8192 fp16 with a
-// residual (470 MB) 81 - 85 us = 5.5 - 5.8 TB/s, 4096 x 4096 24.4 us; fp16 to int8
-// alone, 8192 x 28672 (705 MB) 130 - 141 us = 5.0 - 5.4 TB/s, 30000 x 4000 66 us;
-// one row of 4096 3.5 us against 1.6 us of an empty launch.
+// units stay in registers as they are stored.  MI355X: 8192 x 8192 fp16 with a
+// residual (470 MB) 81 - 87 us = 5.4 - 5.8 TB/s, kept in fp16 instead of int8
+// (537 MB) 95 us, 4096 x 4096 24.4 us; fp16 to int8 alone, 8192 x 28672 (705 MB)
+// 130 - 144 us = 4.9 - 5.4 TB/s, 30000 x 4000 66 us; one row of 4096 3.5 us against
+// 1.6 us of an empty launch.  The norm of up to 8192 columns takes up to 77
+// registers (fp32 103); of more columns its three tensors' units are more than
+// the registers hold (12 spilled at 1024 x 2 in 16 bits, held to eight waves per
+// SIMD; 22 - 36 at 1024 x 4), and it is slower: 4000 x 11008 fp16 81 us =
+// 3.8 TB/s, 2000 x 16384 54 us = 4.3, 1000 x 28672 70 us = 2.9 TB/s.
 //
 // TPR threads per row (64: one wave, several rows to a workgroup), U units of
 // eight elements per thread; the row has at least 8 and at most TPR * U * 8

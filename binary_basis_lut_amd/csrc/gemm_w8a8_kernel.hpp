@@ -194,10 +194,10 @@ __device__ __forceinline__ void wait_and_meet() {
 // lane order.
 //
 // What bounds it: with 256 x 256 tiles the chip's power (8192 x 28672 x 8192 in 1.57
-// - 1.67 ms, 2.3 - 2.45 POP/s; the products alone, on registers, 3.4 POP/s; matrix
+// - 1.71 ms, 2.25 - 2.45 POP/s; the products alone, on registers, 3.4 POP/s; matrix
 // pipes busy 66 % of the cycles at 1.75 GHz), with small tiles the loads that a CU
-// has in flight (about 55 GB/s of operands from HBM and the Infinity Cache, 70
-// with some from L2: 333 x 4096 x 11008 in 29 - 39 us), and for few tokens the HBM
+// has in flight (about 55 GB/s of operands with the weights from HBM, 70
+// where the caches hold them: 333 x 4096 x 11008 in 39 and 29 us), and for few tokens the HBM
 // (16 x 57344 x 8192, 470 MB, at 5.6 TB/s).
 //
 // Fragments are read one step ahead of the products; a step is G of the wave's

@@ -474,8 +474,10 @@ fluxbin_status fluxbin_quantize_rows(const void *x, int64_t ldx, int32_t dtype, 
  * stride.  weight: [cols] in dtype.  The factor inv is common to the row, so
  * the integers do not depend on it.  A row with an infinite or NaN h (or t)
  * gets q = 0 and scale = NaN; where the sum of h^2 is not finite in fp32
- * (fp32 and bf16 rows with values beyond about 1e19) inv is NaN.  eps is
- * finite and >= 0; with eps = 0 a row of zeros has y = NaN and scale = inf. */
+ * (fp32 and bf16 rows with values beyond about 1e19) inv is NaN.  Squares
+ * below fp32's normal range lose bits or count as 0, which shows only where
+ * both they and eps are below about 2^-120.  eps is finite and >= 0; with
+ * eps = 0 a row of zeros has y = NaN and scale = inf. */
 fluxbin_status fluxbin_add_rmsnorm(const void *x, int64_t ldx, const void *residual, int64_t ldr, const void *weight,
                                    int32_t dtype, int64_t rows, int64_t cols, float eps, void *residual_out, int64_t ldro,
                                    void *y, int64_t ldy, int8_t *q, int64_t ldq, float *scale, void *stream);
@@ -500,6 +502,8 @@ fluxbin_status fluxbin_gemm_w8a8(const int8_t *a, int64_t lda, const float *a_sc
  *   top_index[row][0..top_k), top_logprob[row][0..top_k): the top_k largest
  *     logits in descending order, of equal ones the lowest index first, and
  *     their log probabilities.
+ * Differences to the row's largest logit are taken before the scale: one beyond
+ * fp32's range counts as infinite.
  * targets (int64 [rows]) and logprob are both given or both NULL; entropy may
  * be NULL; 0 <= top_k <= min(vocab, 64).  A masked logit (-inf) has
  * probability 0 and log probability -inf and adds 0 to the entropy.  A row
