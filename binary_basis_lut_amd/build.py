@@ -1,9 +1,8 @@
 """Compile libfluxbin.so for gfx950 with hipcc (in-tree, under binary_basis_lut_amd/_build/).
 
 Each translation unit (the host side with the auxiliary kernels, one per table
-width and row-scale format for the GEMV kernel instances, and one per 8-bit
-operator) compiles to
-an object in parallel; the objects link into one shared library.
+width and row-scale format for the GEMV kernel instances, and one per operator
+around the layers) compiles to an object in parallel; the objects link into one shared library.
 """
 from __future__ import annotations
 
@@ -18,10 +17,13 @@ ROOT = PKG.parent
 CSRC = PKG / "csrc"
 SOURCES = [CSRC / "fluxbin.hip"] + [CSRC / f"gemv_g{g}_rs{rs}_t{t}.hip" for g in (4, 8) for rs in (0, 1)
                                    for t in (32, 16)] + [CSRC / "gemv_g8_banked.hip", CSRC / "act_ops.hip",
-                                                      CSRC / "gemm_w8a8.hip", CSRC / "logprobs.hip"]
+                                                      CSRC / "gemm_w8a8.hip", CSRC / "logprobs.hip",
+                                                      CSRC / "rope_append.hip", CSRC / "adjust_logits.hip",
+                                                      CSRC / "paged_attention.hip"]
 HEADERS = [CSRC / "common.hpp", CSRC / "gemv_kernel.hpp", CSRC / "gemv_banked.hpp", CSRC / "aux_kernels.hpp",
            CSRC / "decomp_kernels.hpp", CSRC / "probes.hpp", CSRC / "status.hpp", CSRC / "elements.hpp",
-           CSRC / "wave_ops.hpp",
+           CSRC / "wave_ops.hpp", CSRC / "lds_loads.hpp", CSRC / "paged_batch.hpp", CSRC / "rope_kernels.hpp",
+           CSRC / "adjust_kernels.hpp", CSRC / "attention_kernels.hpp",
            CSRC / "act_kernels.hpp", CSRC / "gemm_w8a8_kernel.hpp", CSRC / "logprob_kernels.hpp", ROOT / "include" / "fluxbin.h"]
 DEPS = SOURCES + HEADERS
 BUILD = PKG / "_build"

@@ -6,6 +6,7 @@
 #pragma once
 
 #include "elements.hpp"
+#include "lds_loads.hpp"
 
 namespace fluxbin {
 
@@ -148,40 +149,6 @@ __global__ __launch_bounds__(64 * KW) void gemm_w8a8_rows_kernel(const GemmArgs 
 }
 
 typedef int32_t i32x16 __attribute__((ext_vector_type(16)));
-
-#define FB_LDS __attribute__((address_space(3)))
-#define FB_GLB __attribute__((address_space(1)))
-
-// Sixteen bytes per lane from global memory straight into LDS: lane l's piece, at
-// base + soff + voff, lands at dst + 16 l.  A buffer load rather than a global
-// one: the compiler takes a direct global load for an LDS access too and would
-// then wait for all fragment reads in flight wherever it waits for some.
-// The same address, known to be the same in every lane: a buffer descriptor in
-// vector registers would be read out lane by lane around every load.
-__device__ __forceinline__ const int8_t *in_scalars(const int8_t *p) {
-  const uint64_t v = reinterpret_cast<uint64_t>(p);
-  return reinterpret_cast<const int8_t *>((uint64_t)(uint32_t)__builtin_amdgcn_readfirstlane((int)(v >> 32)) << 32 |
-                                          (uint32_t)__builtin_amdgcn_readfirstlane((int)v));
-}
-// A buffer of `bytes` 0 gives zeros and touches no memory.
-__device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const int8_t *base, uint32_t bytes) {
-  return __builtin_amdgcn_make_buffer_rsrc(const_cast<int8_t *>(base), 0, bytes, 0x00027000);
-}
-__device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t base, uint32_t voff, uint32_t soff, FB_LDS int8_t *dst) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(base, (FB_LDS void *)dst, 16, voff, soff, 0, 0);
-}
-
-// Waits until at most `vm` of the wave's vector-memory operations and none of
-// its LDS operations are outstanding, then for the workgroup.
-template <int VM>
-__device__ __forceinline__ void wait_and_meet() {
-  static_assert(VM < 64, "vmcnt has six bits");
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_s_waitcnt((VM & 15) | 7 << 4 | (VM >> 4) << 14);  // lgkmcnt 0, expcnt any
-  __builtin_amdgcn_s_barrier();
-  asm volatile("" ::: "memory");
-  __builtin_amdgcn_sched_barrier(0);
-}
 
 // LDS-tiled product: BN channels x BM tokens per workgroup, WN x WM x WK waves
 // (WK of them share a wave tile and split each stage's k), KB bytes of k per

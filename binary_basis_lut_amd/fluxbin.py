@@ -27,6 +27,7 @@ OK, ERR_INVALID_ARGUMENT, ERR_UNSUPPORTED, ERR_WORKSPACE, ERR_HIP = range(5)
 LAYOUT_ROWMAJOR, LAYOUT_TILED = 0, 1
 TABLE_F32, TABLE_F16 = 0, 1
 DT_I8, DT_F16, DT_BITS, DT_BF16, DT_F32 = 0, 1, 2, 3, 4
+ROPE_HALF, ROPE_NEAR = 0, 1
 
 P = ctypes.c_void_p
 I64 = ctypes.c_int64
@@ -56,6 +57,17 @@ class PlanInfo(ctypes.Structure):
 
     def as_dict(self):
         return {name: getattr(self, name) for name, _ in self._fields_}
+
+
+class PagedBatch(ctypes.Structure):
+    """fluxbin_paged_batch: addresses only, the tensors behind them are the caller's to keep."""
+    _fields_ = [
+        ("abi_version", I32), ("dtype", I32), ("heads", I32), ("kv_heads", I32), ("dim", I32), ("page_size", I32),
+        ("tokens", I64), ("seqs", I64), ("max_kv_len", I64),
+        ("seq_starts", P), ("kv_lens", P), ("page_table", P), ("table_ld", I64), ("table_pages", I64),
+        ("k_cache", P), ("v_cache", P),
+        ("cache_pages", I64), ("page_stride", I64), ("head_stride", I64), ("token_stride", I64),
+    ]
 
 
 class FluxbinError(RuntimeError):
@@ -109,6 +121,12 @@ _decl("fluxbin_add_rmsnorm", ctypes.c_int, [P, I64, P, I64, P, I32, I64, I64, FL
 _decl("fluxbin_gemm_w8a8", ctypes.c_int, [P, I64, P, P, I64, P, P, I64, I64, I64, P, I64, I32, P])
 _decl("fluxbin_token_logprobs_workspace_size", ctypes.c_int, [I64, I64, I32, ctypes.POINTER(SIZE_T)])
 _decl("fluxbin_token_logprobs", ctypes.c_int, [P, I64, I32, I64, I64, FLT, P, P, P, I32, P, P, P, SIZE_T, P])
+_decl("fluxbin_rope_append", ctypes.c_int, [ctypes.POINTER(PagedBatch), P, I64, P, I64, P, I64, P, P, FLT, P, I32, I32, FLT, P,
+                                           P, I64, P])
+_decl("fluxbin_paged_attention_workspace_size", ctypes.c_int, [ctypes.POINTER(PagedBatch), ctypes.POINTER(SIZE_T)])
+_decl("fluxbin_paged_attention", ctypes.c_int, [ctypes.POINTER(PagedBatch), P, I64, FLT, I32, P, I64, P, P, SIZE_T, P])
+_decl("fluxbin_adjust_logits", ctypes.c_int, [P, I64, I32, I64, I64, P, I64, I64, P, P, P, P, P, P, P, I64, I64, P, I64, P, I64,
+                                             P])
 
 SYMBOLS = [
     "fluxbin_abi_version", "fluxbin_status_string", "fluxbin_last_error", "fluxbin_tiled_words", "fluxbin_pack",
@@ -122,6 +140,7 @@ SYMBOLS = [
     "fluxbin_decomp_residual_signs", "fluxbin_decomp_error",
     "fluxbin_quantize_rows", "fluxbin_add_rmsnorm", "fluxbin_gemm_w8a8", "fluxbin_token_logprobs_workspace_size",
     "fluxbin_token_logprobs",
+    "fluxbin_rope_append", "fluxbin_paged_attention_workspace_size", "fluxbin_paged_attention", "fluxbin_adjust_logits",
 ]
 
 
@@ -360,6 +379,33 @@ def fluxbin_token_logprobs(logits, ld, dtype, rows, vocab, logit_scale, targets,
     _check(_lib.fluxbin_token_logprobs(_ptr(logits), ld, dtype, rows, vocab, logit_scale, _ptr(targets), _ptr(logprob),
                                        _ptr(entropy), top_k, _ptr(top_logprob), _ptr(top_index), _ptr(workspace),
                                        workspace_bytes, _stream(stream)), "fluxbin_token_logprobs")
+
+
+def fluxbin_rope_append(batch: PagedBatch, q, ldq, k, ldk, v, ldv, q_norm, k_norm, eps, freq, rotary_dim, pairs, rope_scale,
+                        positions, q_out, ldqo, stream=None):
+    _check(_lib.fluxbin_rope_append(batch, _ptr(q), ldq, _ptr(k), ldk, _ptr(v), ldv, _ptr(q_norm), _ptr(k_norm), eps,
+                                    _ptr(freq), rotary_dim, pairs, rope_scale, _ptr(positions), _ptr(q_out), ldqo,
+                                    _stream(stream)), "fluxbin_rope_append")
+
+
+def fluxbin_paged_attention_workspace_size(batch: PagedBatch) -> int:
+    out = SIZE_T(0)
+    _check(_lib.fluxbin_paged_attention_workspace_size(batch, ctypes.byref(out)),
+           "fluxbin_paged_attention_workspace_size")
+    return int(out.value)
+
+
+def fluxbin_paged_attention(batch: PagedBatch, q, ldq, scale, window, out, ldo, lse, workspace, workspace_bytes, stream=None):
+    _check(_lib.fluxbin_paged_attention(batch, _ptr(q), ldq, scale, window, _ptr(out), ldo, _ptr(lse), _ptr(workspace),
+                                        workspace_bytes, _stream(stream)), "fluxbin_paged_attention")
+
+
+def fluxbin_adjust_logits(logits, ld, dtype, rows, vocab, history, ldh, history_cols, prompt_len, total_len, repetition,
+                          frequency, presence, bias_index, bias_value, ldb, biases, mask, ldm, out, ldo, stream=None):
+    _check(_lib.fluxbin_adjust_logits(_ptr(logits), ld, dtype, rows, vocab, _ptr(history), ldh, history_cols, _ptr(prompt_len),
+                                      _ptr(total_len), _ptr(repetition), _ptr(frequency), _ptr(presence), _ptr(bias_index),
+                                      _ptr(bias_value), ldb, biases, _ptr(mask), ldm, _ptr(out), ldo, _stream(stream)),
+           "fluxbin_adjust_logits")
 
 
 def raw_status(name: str, *args) -> int:

@@ -519,6 +519,119 @@ fluxbin_status fluxbin_token_logprobs(const void *logits, int64_t ld, int32_t dt
                                       int32_t top_k, float *top_logprob, int64_t *top_index, void *workspace,
                                       size_t workspace_bytes, void *stream);
 
+/* ------------------------------------------------------------------------
+ * Attention operators: what stands between a layer's QKV product and its
+ * output projection.  The product's rows are normed, rotated and appended to
+ * a paged cache (fluxbin_rope_append), and the new tokens attend to it
+ * (fluxbin_paged_attention); and before a head's logits are scored they are
+ * adjusted (fluxbin_adjust_logits).
+ *
+ * Shared rules: those of the 8-bit operators, and
+ *   - seqs sequences have new tokens, the rows of q, k, v and out in order:
+ *     sequence s has the rows seq_starts[s] .. seq_starts[s + 1] - 1 (int32
+ *     [seqs + 1], not decreasing, from 0 on), or row s alone where seq_starts
+ *     is NULL (then tokens = seqs: a decode step).  Rows behind the last
+ *     sequence are left as they were.
+ *   - kv_lens[s] (int32) is the length of s's cache with its new tokens, so
+ *     that its i-th of n new tokens has the index t = kv_lens[s] - n + i.
+ *   - The cache is cache_pages pages of page_size tokens.  Index t of s is
+ *     token t % page_size of page page_table[s * table_ld + t / page_size]
+ *     (int32, table_pages of them to a sequence).  A page number outside
+ *     [0, cache_pages) is a page that is not there, and so is every index
+ *     from table_pages * page_size on: nothing is stored to it, its keys take
+ *     no part.  No page of a sequence that is appended to is another's.
+ *   - Element d of head h of token i of page p is k_cache[p * page_stride +
+ *     h * head_stride + i * token_stride + d], and likewise in v_cache, so
+ *     that a page may hold its tokens head by head or all heads token by
+ *     token.  Strides are in elements.
+ *   - heads is a multiple of kv_heads: query head h reads key and value head
+ *     h / (heads / kv_heads).  A row of q is heads * dim elements, of k and v
+ *     kv_heads * dim.
+ * All of it but the counts and the strides is read on the device when the
+ * kernels run, so a graph captured once serves every step of a decode.
+ * ------------------------------------------------------------------------ */
+typedef struct {
+  int32_t abi_version;           /* FLUXBIN_ABI_VERSION */
+  int32_t dtype;                 /* of q, k, v, out and the cache: FLUXBIN_DT_F16 or _BF16 */
+  int32_t heads, kv_heads, dim;  /* dim a multiple of 8, at most 256; heads at most 1024 */
+  int32_t page_size;             /* a power of two, 16 .. 65536 */
+  int64_t tokens, seqs;          /* rows of q; sequences.  At most 2^24, and tokens * heads at most 2^30 */
+  int64_t max_kv_len;            /* what no kv_lens[s] passes (0: table_pages * page_size).  It decides how the
+                                    work is divided, not what is computed */
+  const int32_t *seq_starts, *kv_lens, *page_table;
+  int64_t table_ld, table_pages; /* table_ld at least table_pages; table_pages * page_size below 2^31 */
+  void *k_cache, *v_cache;       /* 16-byte aligned */
+  int64_t cache_pages, page_stride, head_stride, token_stride; /* multiples of 8; token_stride dim .. 2^24 */
+} fluxbin_paged_batch;
+
+/* Which elements of a head's first rotary_dim make the pairs of the rotation:
+ * (j, j + rotary_dim / 2), or (2j, 2j + 1). */
+typedef enum { FLUXBIN_ROPE_HALF = 0, FLUXBIN_ROPE_NEAR = 1 } fluxbin_rope_pairs;
+
+/* Queries and new cache entries of every token, in one pass over q, k and v:
+ *   u = x * norm_j / sqrt(mean_j(x_j^2) + eps)  over a head of q (q_norm) or
+ *     k (k_norm), each [dim] in dtype; u = x where that norm is NULL;
+ *   pair j of u's first rotary_dim elements turned by pos * freq[j]:
+ *     (a, b) -> rope_scale * (a cos - b sin, b cos + a sin);
+ *   q_out = round(u) of the queries; round(u) of the keys and v as it is to
+ *     the cache, at the token's index t.
+ * pos is positions[row] (int32 [tokens]), or t where positions is NULL.
+ * freq: double [rotary_dim / 2], the angle per position, whatever scaling of
+ * it a long context asks for; angles are taken in 64 bits, the rest is fp32,
+ * rounded once.  rotary_dim: a multiple of 8 in [0, dim]; 0 rotates nothing
+ * (freq may be NULL).  rope_scale multiplies the rotated elements only.
+ * q may be NULL (keys and values alone), q_out may be q with the same stride.
+ * Queries of a token whose page is not there are written all the same.  A
+ * head whose sum of squares is not finite in fp32 becomes NaN. */
+fluxbin_status fluxbin_rope_append(const fluxbin_paged_batch *batch, const void *q, int64_t ldq, const void *k, int64_t ldk,
+                                   const void *v, int64_t ldv, const void *q_norm, const void *k_norm, float eps,
+                                   const double *freq, int32_t rotary_dim, int32_t pairs, float rope_scale,
+                                   const int32_t *positions, void *q_out, int64_t ldqo, void *stream);
+
+/* Attention of the new tokens over the cache, which holds their own keys and
+ * values already: for the row of index t, with J = the indices j >= 0 that are
+ * there with t - window < j <= t (window 0: j <= t),
+ *   z_j = scale * q . k_j,  lse = log(sum_J exp(z_j)),
+ *   out = sum_J exp(z_j - lse) v_j.
+ * A row without any key (or with z = -inf for all of them) has out = 0 and
+ * lse = -inf.  Keys outside J take no part, whatever they hold, infinities
+ * and NaN too.  lse (fp32 [tokens][heads], natural logarithm) may be NULL; with
+ * it, parts computed apart can be joined.  scale is positive and finite.
+ * Products are taken in dtype's matrix instructions with fp32 sums; the
+ * weights exp(z - max), at most 2^15, are rounded to dtype for the second.
+ * out may not overlap q.  workspace: at least
+ * fluxbin_paged_attention_workspace_size() bytes, 16-byte aligned, free for
+ * other use once the call's work has finished; NULL where that size is 0. */
+fluxbin_status fluxbin_paged_attention_workspace_size(const fluxbin_paged_batch *batch, size_t *bytes);
+fluxbin_status fluxbin_paged_attention(const fluxbin_paged_batch *batch, const void *q, int64_t ldq, float scale, int32_t window,
+                                       void *out, int64_t ldo, float *lse, void *workspace, size_t workspace_bytes,
+                                       void *stream);
+
+/* Logits x [rows][vocab] made ready for a choice among them.  With the row's
+ * tokens so far, history[row][0 .. total_len[row]), of which the first
+ * prompt_len[row] were given and the others generated, and c_j the number of
+ * times that token j was generated:
+ *   z = x > 0 ? x / repetition : x * repetition   for tokens of the history,
+ *   z = z - frequency * c_j - presence * [c_j > 0],
+ *   z = z + the sum, in their order, of the bias_value whose bias_index is j,
+ *   z = -inf where bit j % 32 of mask[row][j / 32] is 0,
+ * rounded once to dtype.  history int32 [rows][ldh], of which history_cols
+ * columns exist; total_len and prompt_len int32 [rows] (NULL: history_cols,
+ * and 0), taken into [0, history_cols]; repetition (> 0), frequency, presence fp32
+ * [rows] (NULL: 1, 0, 0); bias_index int32, bias_value fp32 [rows][ldb], of
+ * which `biases` (at most 4096) columns exist; mask uint32 [rows][ldm], least
+ * significant bit first as in the sign words, NULL: everything allowed.
+ * Tokens and bias indices outside [0, vocab) count as absent.  history NULL
+ * with history_cols 0: no penalties; bias_index NULL with biases 0: no
+ * biases.  out may be logits with the same stride, or not overlap it.
+ * dtype fp16, bf16 or fp32; rows <= 2^22, vocab <= 2^28, history_cols <=
+ * 2^30. */
+fluxbin_status fluxbin_adjust_logits(const void *logits, int64_t ld, int32_t dtype, int64_t rows, int64_t vocab,
+                                     const int32_t *history, int64_t ldh, int64_t history_cols, const int32_t *prompt_len,
+                                     const int32_t *total_len, const float *repetition, const float *frequency,
+                                     const float *presence, const int32_t *bias_index, const float *bias_value, int64_t ldb,
+                                     int64_t biases, const uint32_t *mask, int64_t ldm, void *out, int64_t ldo, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
