@@ -4,9 +4,12 @@
 // running maximum m (of the s_j seen) and
 //     p_j = 2^(c s_j - c m + 7),  l = sum p_j,  o = sum p_j v_j,
 // keys come in tiles; where a tile raises m, l and o are multiplied with
-// 2^(c (m_old - m_new)).  out = o / l, lse = ln2 (c m - 7 + log2 l).  The factor 2^7
-// keeps small weights out of fp16's subnormals.  Two sets of keys are joined in
-// the same way, so keys may be split over waves and workgroups.
+// 2^(c (m_old - m_new)).  out = o / l, lse = ln2 (c m - 7 + log2 l).  m is raised only
+// when a score passes it by more than kSlack (in powers of two), so weights reach
+// 2^15; the factor 2^7 keeps small ones out of fp16's subnormals.  Weights are
+// rounded to the activation type for the second product alone: l, and with it lse,
+// is the fp32 sum of the weights before that.  Two sets of keys are joined by moving both to the larger m, so keys
+// may be split over waves and workgroups.
 //
 // All rows that read one key head are rows of one matrix: row r of a sequence is
 // query head r % G of its group of G and token r / G.  Both products run
@@ -49,7 +52,7 @@ struct AttentionArgs {
   float c;
 };
 
-constexpr float kWeightShift = 7.0f;
+constexpr float kWeightShift = 7.0f, kSlack = 8.0f;
 
 template <typename E>
 __device__ __forceinline__ f32x16 multiply(u32x4 a, u32x4 b, f32x16 acc);
@@ -63,9 +66,18 @@ __device__ __forceinline__ f32x16 multiply<BF16>(u32x4 a, u32x4 b, f32x16 acc) {
 }
 
 // Two values rounded to nearest even, the first in the low half.
+typedef float f32x2 __attribute__((ext_vector_type(2)));
+typedef _Float16 f16x2 __attribute__((ext_vector_type(2)));
+typedef __bf16 bf16x2 __attribute__((ext_vector_type(2)));
 template <typename E>
-__device__ __forceinline__ uint32_t pair_of(float x, float y) {
-  return (uint32_t)E::round(x) | (uint32_t)E::round(y) << 16;
+__device__ __forceinline__ uint32_t pair_of(float x, float y);
+template <>
+__device__ __forceinline__ uint32_t pair_of<F16>(float x, float y) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x, y}, f16x2));
+}
+template <>
+__device__ __forceinline__ uint32_t pair_of<BF16>(float x, float y) {
+  return __builtin_bit_cast(uint32_t, __builtin_convertvector(f32x2{x, y}, bf16x2));
 }
 
 // A lane's value and that of the lane 32 away, the lower lane's first.  The second
@@ -209,13 +221,8 @@ struct WaveTile {
     }
   }
 
-  // there: bit g says that the tile's group g of 16 keys has a page; all of them
-  // and no border of anybody's view inside the tile: masked = false.  mixed: the
-  // tile has keys that some rows see and others do not.
-  __device__ __forceinline__ void take(const AttentionArgs &a, const int8_t *kt, const int8_t *vt, int key0, bool masked, bool mixed,
-                                       uint32_t there, int lane) {
-    const int half = lane / 32;
-    f32x16 s[KB][QB];
+  // S^T of the tile.
+  __device__ __forceinline__ void scores(const int8_t *kt, int lane, f32x16 (&s)[KB][QB]) const {
 #pragma unroll
     for (int k = 0; k < KB; ++k) {
 #pragma unroll
@@ -223,57 +230,59 @@ struct WaveTile {
 #pragma unroll
       for (int i = 0; i < STEPS; ++i) {
         const int row = 32 * k + lane % 32;
-        const u32x4 f = *reinterpret_cast<const u32x4 *>(kt + row * D * 2 + k_place<D>(row, 2 * i + half) * 16);
+        const u32x4 f = *reinterpret_cast<const u32x4 *>(kt + row * D * 2 + k_place<D>(row, 2 * i + lane / 32) * 16);
 #pragma unroll
         for (int x = 0; x < QB; ++x) s[k][x] = multiply<E>(f, q[x][i], s[k][x]);
       }
     }
-    if (masked) {
-#pragma unroll
-      for (int k = 0; k < KB; ++k)
-#pragma unroll
-        for (int x = 0; x < QB; ++x)
-#pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int key = key0 + 32 * k + 8 * (i / 4) + 4 * half + i % 4;
-            const bool seen = key >= from[x] && key <= p[x] && (there >> (2 * k + i / 8) & 1);
-            s[k][x][i] = seen ? s[k][x][i] : -__builtin_inff();
-          }
-    }
-    u32x4 w[KB][2][QB];  // the weights, 16 keys to an operand
+  }
+
+  // Scores to weights, with what that does to m, l and o.
+  __device__ __forceinline__ void weights(float c, f32x16 (&s)[KB][QB], u32x4 (&w)[KB][2][QB]) {
+    float top[QB];
+    bool rise = false;
 #pragma unroll
     for (int x = 0; x < QB; ++x) {
-      float top = s[0][x][0];
+      top[x] = s[0][x][0];
 #pragma unroll
       for (int k = 0; k < KB; ++k)
 #pragma unroll
-        for (int i = 0; i < 16; ++i) top = fmaxf(top, s[k][x][i]);
-      top = fmaxf(m[x], other_half_max(top));
-      const float base = top == -__builtin_inff() ? 0.0f : top;
-      const float factor = __builtin_amdgcn_exp2f((m[x] - base) * a.c), shift = kWeightShift - base * a.c;
-      m[x] = top;
-      float sum = 0.0f;
+        for (int i = 0; i < 16; ++i) top[x] = fmaxf(top[x], s[k][x][i]);
+      top[x] = other_half_max(top[x]);
+      rise = rise || (top[x] - m[x]) * c > kSlack || (m[x] == -__builtin_inff() && top[x] != m[x]);
+    }
+    if (__any(rise)) {
 #pragma unroll
-      for (int k = 0; k < KB; ++k)
+      for (int x = 0; x < QB; ++x) {
+        const float up = fmaxf(m[x], top[x]);
+        float factor = up == -__builtin_inff() ? 1.0f : __builtin_amdgcn_exp2f((m[x] - up) * c);
+        asm volatile("" : "+v"(factor));
+        m[x] = up;
+        l[x] *= factor;
 #pragma unroll
-        for (int i = 0; i < 16; ++i) {
-          s[k][x][i] = __builtin_amdgcn_exp2f(fmaf(s[k][x][i], a.c, shift));
-          sum += s[k][x][i];
-        }
-      l[x] = fmaf(l[x], factor, sum);
+        for (int i = 0; i < DB; ++i) o[i][x] *= factor;
+      }
+    }
+#pragma unroll
+    for (int x = 0; x < QB; ++x) {
+      const float shift = m[x] == -__builtin_inff() ? 0.0f : kWeightShift - m[x] * c;
+      float sum[2] = {0.0f, 0.0f};
 #pragma unroll
       for (int k = 0; k < KB; ++k)
 #pragma unroll
         for (int j = 0; j < 2; ++j)
 #pragma unroll
-          for (int i = 0; i < 4; ++i) w[k][j][x][i] = pair_of<E>(s[k][x][8 * j + 2 * i], s[k][x][8 * j + 2 * i + 1]);
-#pragma unroll
-      for (int i = 0; i < DB; ++i) o[i][x] *= factor;
+          for (int i = 0; i < 4; ++i) {
+            const float a = __builtin_amdgcn_exp2f(fmaf(s[k][x][8 * j + 2 * i], c, shift));
+            const float b = __builtin_amdgcn_exp2f(fmaf(s[k][x][8 * j + 2 * i + 1], c, shift));
+            w[k][j][x][i] = pair_of<E>(a, b);
+            sum[i % 2] += a + b;
+          }
+      l[x] += sum[0] + sum[1];
     }
-    if (mixed && unclean(vt, lane)) {
-      one_by_one(vt, w, lane);
-      return;
-    }
+  }
+
+  __device__ __forceinline__ void add_values(const int8_t *vt, int lane, const u32x4 (&w)[KB][2][QB]) {
 #pragma unroll
     for (int k = 0; k < KB; ++k)
 #pragma unroll
@@ -284,6 +293,32 @@ struct WaveTile {
 #pragma unroll
           for (int x = 0; x < QB; ++x) o[i][x] = multiply<E>(v, w[k][j][x], o[i][x]);
         }
+  }
+
+  // The tile that begins at key0.  part: the border of a row's view lies in it, or
+  // keys that are not there (bit g of `there`: its group g of 16 has a page).
+  // (The empty asm makes a value of the rare work known there only, which keeps the
+  // compiler from doing that work always.)
+  __device__ __forceinline__ void take(float c, const int8_t *kt, const int8_t *vt, bool part, int key0, uint32_t there, int lane) {
+    f32x16 s[KB][QB];
+    u32x4 w[KB][2][QB];
+    scores(kt, lane, s);
+    if (part) {
+      int mine = key0 + 4 * (lane / 32);
+      asm volatile("" : "+v"(mine));
+#pragma unroll
+      for (int k = 0; k < KB; ++k)
+#pragma unroll
+        for (int x = 0; x < QB; ++x)
+#pragma unroll
+          for (int i = 0; i < 16; ++i) {
+            const int key = mine + 32 * k + 8 * (i / 4) + i % 4;
+            const bool seen = key >= from[x] && key <= p[x] && (there >> (2 * k + i / 8) & 1);
+            s[k][x][i] = seen ? s[k][x][i] : -__builtin_inff();
+          }
+    }
+    weights(c, s, w);
+    add_values(vt, lane, w);
   }
 
   // V^T of dimensions 32 i .. + 31 and 16 keys in the order of the weights: lane l
@@ -314,53 +349,91 @@ struct WaveTile {
     }
     return __any(bad);
   }
-
-  // The second product where such values stand among keys that not every row
-  // sees: key by key, a row leaving out those whose weight is 0.
-  __device__ __forceinline__ void one_by_one(const int8_t *vt, const u32x4 (&w)[KB][2][QB], int lane) {
-#pragma unroll 1
-    for (int key = 0; key < KT; ++key) {
-      const int hold = key / 4 % 2;  // which half of the wave has its weights, and where
-      const int pick = key / 32 * 16 + key % 32 / 8 * 4 + key % 4;
-#pragma unroll
-      for (int x = 0; x < QB; ++x) {
-        uint32_t word = 0;
-#pragma unroll
-        for (int i = 0; i < KB * 8; ++i) word = pick / 2 == i ? w[i / 8][i / 4 % 2][x][i % 4] : word;
-        word = __shfl(word, lane % 32 + 32 * hold);
-        const float f = E::load((uint16_t)(word >> (16 * (pick % 2))));
-        if (f != 0.0f) {
-#pragma unroll
-          for (int i = 0; i < DB; ++i)
-#pragma unroll
-            for (int j = 0; j < 4; ++j) {
-              const u32x2 v = *reinterpret_cast<const u32x2 *>(vt + key * D * 2 + v_place<D>(key, 4 * i + j) * 16 + lane / 32 * 8);
-#pragma unroll
-              for (int e = 0; e < 4; ++e)
-                o[i][x][4 * j + e] = fmaf(f, E::load((uint16_t)(v[e / 2] >> (16 * (e % 2)))), o[i][x][4 * j + e]);
-            }
-        }
-      }
-    }
-  }
 };
 
-// What a row comes to: its output and lse, or the part of a split.  v: elements
-// d .. d + 3 of o.
+// What a row comes to: its output and lse, or the part of a split.
 __device__ __forceinline__ float lse_of(float cm, float l) {
   return l == 0.0f ? -__builtin_inff() : 0.69314718055994530942f * (cm - kWeightShift + log2f(l));
 }
+struct Place {
+  uint16_t *out;
+  float *part;  // null where the keys are not split
+  float inv;
+  template <typename E>
+  __device__ __forceinline__ void put(int d, f32x4 o) const {
+    if (part) *reinterpret_cast<f32x4 *>(part + d) = o;
+    else *reinterpret_cast<words2 *>(out + d) = words2{pair_of<E>(o[0] * inv, o[1] * inv), pair_of<E>(o[2] * inv, o[3] * inv)};
+  }
+};
+
+// Where a row's o goes; its lse, or the split's (c m, l), is written here by the
+// lane that is `first` of those that have the row.
+__device__ __forceinline__ Place place_of(const AttentionArgs &a, const Rows &r, int head, int row, int split, float cm, float l, bool first) {
+  const int64_t at = (int64_t)(r.start + row / a.group) * a.b.heads + head * a.group + row % a.group;
+  Place p;
+  p.out = a.out + (int64_t)(r.start + row / a.group) * a.ldo + (head * a.group + row % a.group) * a.b.dim;
+  p.part = a.splits > 1 ? a.part + (at * a.splits + split) * a.b.dim : nullptr;
+  p.inv = l == 0.0f ? 0.0f : 1.0f / l;
+  if (first && a.splits > 1) {
+    a.part[a.parts * a.b.dim + 2 * (at * a.splits + split)] = cm;
+    a.part[a.parts * a.b.dim + 2 * (at * a.splits + split) + 1] = l;
+  } else if (first && a.lse) {
+    a.lse[at] = lse_of(cm, l);
+  }
+  return p;
+}
+
+// Rows [from, to) of a workgroup over the keys [k0, k1), one after the other by a
+// wave: 64 keys at a time, a lane to a key, then a lane to four dimensions.  For
+// infinities and NaN among values that some rows see and others do not, which a
+// matrix product would carry to all of them (0 times infinity): here a key whose
+// weight is 0 is left out.
 template <typename E>
-__device__ __forceinline__ void put_out(const AttentionArgs &a, int64_t token, int head, int d, f32x4 v, float inv) {
-  *reinterpret_cast<words2 *>(a.out + token * a.ldo + head * a.b.dim + d) =
-      words2{pair_of<E>(v[0] * inv, v[1] * inv), pair_of<E>(v[2] * inv, v[3] * inv)};
+__device__ __forceinline__ void rows_one_by_one(const AttentionArgs &a, const Rows &r, int head, int split, int from, int to, int step, int k0,
+                                         int k1, int lane) {
+  const Paged &b = a.b;
+  for (int row = from; row < to; row += step) {
+    const int token = row / a.group, p = r.before + token, first = a.window ? max(0, p - a.window + 1) : 0;
+    const uint16_t *q = a.q + (int64_t)(r.start + token) * a.ldq + (head * a.group + row % a.group) * b.dim;
+    float m = -__builtin_inff(), l = 0.0f;
+    f32x4 o{0, 0, 0, 0};
+    for (int base = max(k0, first); base < min(k1, p + 1); base += 64) {
+      const int key = base + lane;
+      int page = -1;
+      if (key < k1 && key <= p) page = page_of(b, r.seq, key);
+      const int64_t at = (int64_t)page * b.page_stride + (int64_t)head * b.head_stride +
+                         (int64_t)(key & ((1 << b.page_shift) - 1)) * b.token_stride;
+      float s = -__builtin_inff();
+      if (page >= 0) {
+        s = 0.0f;
+        for (int d = 0; d < b.dim; ++d) s = fmaf(E::load(b.k[at + d]), E::load(q[d]), s);
+      }
+      const float top = fmaxf(m, wave_reduce<MaxF>(s));
+      if (__any(s != s)) l = __builtin_nanf("");
+      if (top == -__builtin_inff()) continue;
+      const float factor = __builtin_amdgcn_exp2f((m - top) * a.c);
+      m = top;
+      const float w = __builtin_amdgcn_exp2f(fmaf(s, a.c, kWeightShift - m * a.c));
+      l = fmaf(l, factor, wave_reduce<SumF>(w));
+      o *= factor;
+      for (int j = 0; j < 64; ++j) {
+        const float wj = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), j));
+        if (wj == 0.0f) continue;
+        const int64_t v = (int64_t)__shfl((int)(at >> 32), j) << 32 | (uint32_t)__shfl((int)at, j);
+        if (4 * lane < b.dim)
+          for (int i = 0; i < 4; ++i) o[i] = fmaf(wj, E::load(b.v[v + 4 * lane + i]), o[i]);
+      }
+    }
+    const Place place = place_of(a, r, head, row, split, m * a.c, l, lane == 0);
+    if (4 * lane < b.dim) place.put<E>(4 * lane, o);
+  }
 }
 
 // 128 x QB rows, 32 x QB to each of four waves, over one split of their keys; a
 // workgroup's tiles of KT keys come by two buffers, the next one loaded while one is
 // worked on.
 template <typename E, int D, int QB>
-__global__ __launch_bounds__(256) void attention_chunk_kernel(const AttentionArgs a) {
+__global__ __launch_bounds__(256, 2) void attention_chunk_kernel(const AttentionArgs a) {
   constexpr int BM = 128 * QB, KT = D == 256 ? 32 : 64, GROUPS = KT / 16, JOBS = 2 * GROUPS / 4, BYTES = KT * D * 2;
   typedef GroupLoads<D> Loads;
   __shared__ __align__(1024) int8_t lds[2][2][BYTES];  // [buffer][K, V]
@@ -398,46 +471,36 @@ __global__ __launch_bounds__(256) void attention_chunk_kernel(const AttentionArg
   uint32_t there = there_of();
   if (t0 < t1) fetch(t0, 0);
   find_pages(t0 + 1);
+  const int first_row = r.first + wave * 32 * QB, end_row = min(first_row + 32 * QB, r.count);
+  bool bad = false;
   for (int t = t0; t < t1; ++t) {
-    const int buf = (t - t0) % 2;
+    const int buf = (t - t0) % 2, key0 = t * KT;
     wait_and_meet<0>();
-    const uint32_t next = there_of();
+    const uint32_t now = there;
+    there = there_of();
     if (t + 1 < t1) fetch(t + 1, buf ^ 1);
     find_pages(t + 2);
-    const int key0 = t * KT;
     const bool border = key0 + KT - 1 > r.p_lo || (a.window && key0 <= r.p_hi - a.window);
-    w.take(a, lds[buf][0], lds[buf][1], key0, border || there != (1u << GROUPS) - 1 || key0 + KT > r.hi, border && r.p_lo != r.p_hi,
-           there, lane);
-    there = next;
+    if (border && r.p_lo != r.p_hi) bad = bad || w.unclean(lds[buf][1], lane);
+    w.take(a.c, lds[buf][0], lds[buf][1], border || now != (1u << GROUPS) - 1 || key0 + KT > r.hi, key0, now, lane);
   }
-
+  if (bad) {
+    rows_one_by_one<E>(a, r, head, split, first_row, end_row, 1, t0 * KT, t1 * KT, lane);
+    return;
+  }
 #pragma unroll
   for (int x = 0; x < QB; ++x) {
-    const int row = r.first + (wave * QB + x) * 32 + lane % 32;
-    if (row >= r.count) continue;
-    const float l = other_half_sum(w.l[x]), cm = w.m[x] * a.c;
-    const int64_t token = r.start + row / a.group;
-    const int h = head * a.group + row % a.group;
-    const int64_t at = (token * b.heads + h) * a.splits + split;
-    const float inv = l == 0.0f ? 0.0f : 1.0f / l;
-    if (lane < 32) {
-      if (a.splits > 1) {
-        a.part[a.parts * b.dim + 2 * at] = cm;
-        a.part[a.parts * b.dim + 2 * at + 1] = l;
-      } else if (a.lse) {
-        a.lse[token * b.heads + h] = lse_of(cm, l);
-      }
-    }
+    const int row = first_row + 32 * x + lane % 32;
+    const float l = other_half_sum(w.l[x]);
+    if (row >= end_row) continue;
+    const Place place = place_of(a, r, head, row, split, w.m[x] * a.c, l, lane < 32);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
         const int d = 32 * i + 8 * j + 4 * (lane / 32);
-        const f32x4 v{w.o[i][x][4 * j], w.o[i][x][4 * j + 1], w.o[i][x][4 * j + 2], w.o[i][x][4 * j + 3]};
-        if (d < b.dim) {
-          if (a.splits > 1) *reinterpret_cast<f32x4 *>(a.part + at * b.dim + d) = v;
-          else put_out<E>(a, token, h, d, v, inv);
-        }
+        if (d < b.dim)
+          place.put<E>(d, f32x4{w.o[i][x][4 * j], w.o[i][x][4 * j + 1], w.o[i][x][4 * j + 2], w.o[i][x][4 * j + 3]});
       }
   }
 }
@@ -457,6 +520,7 @@ __global__ __launch_bounds__(64 * Few<D>::W) void attention_few_kernel(const Att
   static_assert(W * 32 * ROW * 4 <= W * S * 2 * BYTES, "the waves' sums take the place of the tiles");
   __shared__ __align__(1024) int8_t lds[W * S * 2 * BYTES];
   __shared__ float stats[2][W][32];
+  __shared__ bool any_bad[W];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
   const Paged &b = a.b;
   const int head = blockIdx.x % b.kv_heads, rest = blockIdx.x / b.kv_heads;
@@ -495,12 +559,13 @@ __global__ __launch_bounds__(64 * Few<D>::W) void attention_few_kernel(const Att
       Loads::load(group_of(b, b.v, head, t * KT + 16 * g, page, r), lane, off_v, (FB_LDS int8_t *)dst + BYTES + g * 16 * D * 2);
     }
   };
+  bool bad = false;
   const auto work = [&](int t, int stage) {
     const int key0 = t * KT;
     const int8_t *from = mine + stage * 2 * BYTES;
     const bool border = key0 + KT - 1 > r.p_lo || (a.window && key0 <= r.p_hi - a.window);
-    w.take(a, from, from + BYTES, key0, border || there[stage] != 3 || key0 + KT > r.hi, border && r.p_lo != r.p_hi, there[stage],
-           lane);
+    if (border && r.p_lo != r.p_hi) bad = bad || w.unclean(from + BYTES, lane);
+    w.take(a.c, from, from + BYTES, border || there[stage] != 3 || key0 + KT > r.hi, key0, there[stage], lane);
   };
 #pragma unroll
   for (int i = 0; i < S; ++i) fetch(i, i);
@@ -522,7 +587,15 @@ __global__ __launch_bounds__(64 * Few<D>::W) void attention_few_kernel(const Att
     stats[0][wave][lane] = w.m[0];
     stats[1][wave][lane] = l;
   }
+  if (lane == 0) any_bad[wave] = bad;
   __syncthreads();
+  const int rows = min(32, r.count - r.first);
+#pragma unroll
+  for (int v = 0; v < W; ++v) bad = bad || any_bad[v];
+  if (bad) {
+    rows_one_by_one<E>(a, r, head, split, r.first + wave, r.first + rows, W, t0 * KT, t1 * KT, lane);
+    return;
+  }
   const int mine_row = lane % 32;
   float top = -__builtin_inff();
 #pragma unroll
@@ -536,7 +609,6 @@ __global__ __launch_bounds__(64 * Few<D>::W) void attention_few_kernel(const Att
       *reinterpret_cast<f32x4 *>(sums + (wave * 32 + mine_row) * ROW + 32 * i + 8 * j + 4 * (lane / 32)) =
           f32x4{w.o[i][0][4 * j], w.o[i][0][4 * j + 1], w.o[i][0][4 * j + 2], w.o[i][0][4 * j + 3]} * factor;
   __syncthreads();
-  const int rows = min(32, r.count - r.first);
   for (int x = threadIdx.x; x < rows * (D / 4); x += 64 * W) {
     const int row = x / (D / 4), d = x % (D / 4) * 4;
     if (d >= b.dim) continue;
@@ -551,19 +623,7 @@ __global__ __launch_bounds__(64 * Few<D>::W) void attention_few_kernel(const Att
       sum = fmaf(stats[1][v][row], __builtin_amdgcn_exp2f((m - big) * a.c), sum);
       o += *reinterpret_cast<const f32x4 *>(sums + (v * 32 + row) * ROW + d);
     }
-    const int64_t token = r.start + (r.first + row) / a.group;
-    const int h = head * a.group + (r.first + row) % a.group;
-    const int64_t at = (token * b.heads + h) * a.splits + split;
-    if (a.splits > 1) {
-      *reinterpret_cast<f32x4 *>(a.part + at * b.dim + d) = o;
-      if (d == 0) {
-        a.part[a.parts * b.dim + 2 * at] = big * a.c;
-        a.part[a.parts * b.dim + 2 * at + 1] = sum;
-      }
-    } else {
-      put_out<E>(a, token, h, d, o, sum == 0.0f ? 0.0f : 1.0f / sum);
-      if (a.lse && d == 0) a.lse[token * b.heads + h] = lse_of(big * a.c, sum);
-    }
+    place_of(a, r, head, r.first + row, split, big * a.c, sum, d == 0).put<E>(d, o);
   }
 }
 
@@ -589,7 +649,8 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttentionArgs
     const float fs = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), s));
     if (fs != 0.0f && 4 * lane < b.dim) o += *reinterpret_cast<const f32x4 *>(a.part + (row * a.splits + s) * b.dim + 4 * lane) * fs;
   }
-  if (4 * lane < b.dim) put_out<E>(a, token, (int)(row % b.heads), 4 * lane, o, sum == 0.0f ? 0.0f : 1.0f / sum);
+  const Place place{a.out + (int64_t)token * a.ldo + row % b.heads * b.dim, nullptr, sum == 0.0f ? 0.0f : 1.0f / sum};
+  if (4 * lane < b.dim) place.put<E>(4 * lane, o);
   if (a.lse && lane == 0) a.lse[row] = lse_of(top, sum);
 }
 

@@ -162,7 +162,7 @@ def test_what_a_row_does_not_see_does_not_matter(fb, dt, dim, heads, kv, lengths
     scale = 1 / math.sqrt(dim)
     clean, ls_clean = attend(fb, c, scale, window)
     out, _, mag, work, seen = attention_oracle(c, scale, window)
-    tol, _ = attention_bounds(c, out, mag, work, seen)
+    tol, tol_lse = attention_bounds(c, out, mag, work, seen)
     mine = np.zeros((c.pages, c.page), dtype=bool)
     for s in range(len(lengths)):
         for j in range(c.lens_host[s]):
@@ -182,9 +182,10 @@ def test_what_a_row_does_not_see_does_not_matter(fb, dt, dim, heads, kv, lengths
         others = np.arange(c.rows) != row
         want = clean.copy()
         want[row, :, dim // 2] = bad[which].item()
-        # added key by key: another order of the same sum, so both are within the bound of the definition
+        # computed key by key, products and sums in another order: both are within their bounds of the definition, so within
+        # twice those of each other
         assert ((np.abs(got - want) <= 2 * tol) | (np.isnan(got) & np.isnan(want)) | (got == want)).all()
-        assert np.isfinite(got[others]).all() and np.array_equal(ls, ls_clean)
+        assert np.isfinite(got[others]).all() and (np.abs(ls - ls_clean) <= 2 * (tol_lse + 4 * U * np.abs(ls_clean))).all()
     c.k[c.table_host[0, last // 32], :, last % 32, 3] = math.nan
     got, ls = attend(fb, c, scale, window)
     assert np.isnan(got[row]).all() and np.isnan(ls[row]).all() and np.isfinite(got[others]).all()
