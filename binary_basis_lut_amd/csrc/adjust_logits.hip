@@ -6,19 +6,25 @@ using namespace fluxbin;
 
 namespace {
 
-constexpr int64_t kMaxRows = (int64_t)1 << 22, kMaxVocab = (int64_t)1 << 28, kMaxHistory = (int64_t)1 << 30, kMaxBiases = 4096;
+constexpr int64_t kMaxRows = (int64_t)1 << 22, kMaxVocab = (int64_t)1 << 28, kMaxHistory = ((int64_t)1 << 30) - 1, kMaxBiases = 4096;
 
-template <typename E, bool TINY>
+constexpr int64_t kShort = 4096;  // tokens of a row that one workgroup of 256 threads takes
+
+int64_t slice_of(int64_t vocab, int64_t biases) { return vocab <= kShort ? kShort : biases ? 8192 : 16384; }
+
+template <typename E, bool BIAS, bool TINY, int T, int SLICE>
 void launch(const AdjustArgs &a, hipStream_t st) {
-  const dim3 grid((unsigned)(a.rows * a.slices)), block(256);
-  if (a.biases) hipLaunchKernelGGL((adjust_logits_kernel<E, true, TINY>), grid, block, 0, st, a);
-  else hipLaunchKernelGGL((adjust_logits_kernel<E, false, TINY>), grid, block, 0, st, a);
+  hipLaunchKernelGGL((adjust_logits_kernel<E, BIAS, TINY, T, SLICE>), dim3((unsigned)(a.rows * a.slices)), dim3(T), 0, st, a);
 }
 
 template <typename E>
 void run(const AdjustArgs &a, hipStream_t st) {
-  if (a.vocab < kUnit) launch<E, true>(a, st);
-  else launch<E, false>(a, st);
+  if (a.vocab < kUnit && a.biases) launch<E, true, true, 256, kShort>(a, st);
+  else if (a.vocab < kUnit) launch<E, false, true, 256, kShort>(a, st);
+  else if (a.vocab <= kShort && a.biases) launch<E, true, false, 256, kShort>(a, st);
+  else if (a.vocab <= kShort) launch<E, false, false, 256, kShort>(a, st);
+  else if (a.biases) launch<E, true, false, 1024, 8192>(a, st);
+  else launch<E, false, false, 1024, 16384>(a, st);
 }
 
 }  // namespace
@@ -37,11 +43,11 @@ extern "C" fluxbin_status fluxbin_adjust_logits(const void *logits, int64_t ld, 
   if (history_cols < 0 || biases < 0)
     return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "history_cols = %lld, biases = %lld", (long long)history_cols, (long long)biases);
   if (history_cols > kMaxHistory || biases > kMaxBiases)
-    return fail(FLUXBIN_ERR_UNSUPPORTED, "history_cols above 2^30 or more than %lld biases", (long long)kMaxBiases);
+    return fail(FLUXBIN_ERR_UNSUPPORTED, "history_cols from 2^30 on or more than %lld biases", (long long)kMaxBiases);
   if (rows == 0) return ok();
   const int bytes = dtype == FLUXBIN_DT_F32 ? 4 : 2;
-  const int64_t slices = cdiv(vocab, kAdjustSlice);
-  if (rows * slices >= (int64_t)1 << 24)
+  const int64_t slices = cdiv(vocab, slice_of(vocab, biases));
+  if (rows * slices >= (int64_t)1 << 22)
     return fail(FLUXBIN_ERR_UNSUPPORTED, "%lld rows of %lld tokens are beyond one launch", (long long)rows, (long long)vocab);
   if (!logits || !out) return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "logits or out is NULL");
   if (ld < vocab || ldo < vocab)

@@ -454,9 +454,19 @@ __global__ __launch_bounds__(256, 2) void attention_chunk_kernel(const Attention
   uint32_t off[JOBS][Loads::kLoads];
 #pragma unroll
   for (int j = 0; j < JOBS; ++j) Loads::offsets(b, lane, (j * 4 + wave) / GROUPS, off[j]);
-  // lane g of `pages`: the page of the group g of the tile that is fetched next
+  // lane i: the page of group i of the tile that is fetched next.  The number is looked
+  // at a tile later than it is asked for (the asm keeps the compiler from looking at
+  // once), since a wait for it is a wait for all loads before it.
   int pages;
-  const auto find_pages = [&](int t) { pages = t < t1 ? page_of(b, r.seq, t * KT + 16 * (lane % GROUPS)) : -1; };
+  const auto find_pages = [&](int t) {
+    const int i = (t * KT + 16 * (lane % GROUPS)) >> b.page_shift;
+    pages = -1;
+    if (t < t1 && i < b.table_pages) pages = b.page_table[(int64_t)r.seq * b.table_ld + i];
+  };
+  const auto settle = [&]() {
+    asm volatile("" : "+v"(pages));
+    pages = (uint32_t)pages < (uint32_t)b.pages ? pages : -1;
+  };
   const auto there_of = [&]() { return (uint32_t)__ballot(pages >= 0) & ((1u << GROUPS) - 1); };
   const auto fetch = [&](int t, int buf) {
 #pragma unroll
@@ -468,6 +478,7 @@ __global__ __launch_bounds__(256, 2) void attention_chunk_kernel(const Attention
     }
   };
   find_pages(t0);
+  settle();
   uint32_t there = there_of();
   if (t0 < t1) fetch(t0, 0);
   find_pages(t0 + 1);
@@ -477,6 +488,7 @@ __global__ __launch_bounds__(256, 2) void attention_chunk_kernel(const Attention
     const int buf = (t - t0) % 2, key0 = t * KT;
     wait_and_meet<0>();
     const uint32_t now = there;
+    settle();
     there = there_of();
     if (t + 1 < t1) fetch(t + 1, buf ^ 1);
     find_pages(t + 2);

@@ -624,8 +624,8 @@ fluxbin_status fluxbin_paged_attention(const fluxbin_paged_batch *batch, const v
  * Tokens and bias indices outside [0, vocab) count as absent.  history NULL
  * with history_cols 0: no penalties; bias_index NULL with biases 0: no
  * biases.  out may be logits with the same stride, or not overlap it.
- * dtype fp16, bf16 or fp32; rows <= 2^22, vocab <= 2^28, history_cols <=
- * 2^30. */
+ * dtype fp16, bf16 or fp32; vocab <= 2^28, rows *
+ * ceil(vocab / 8192) below 2^22, history_cols below 2^30. */
 fluxbin_status fluxbin_adjust_logits(const void *logits, int64_t ld, int32_t dtype, int64_t rows, int64_t vocab,
                                      const int32_t *history, int64_t ldh, int64_t history_cols, const int32_t *prompt_len,
                                      const int32_t *total_len, const float *repetition, const float *frequency,
