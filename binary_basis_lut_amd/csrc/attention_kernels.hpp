@@ -177,12 +177,13 @@ struct GroupLoads {
       off[i] = piece * 8 < b.dim ? (uint32_t)(row * b.token_stride * 2 + piece * 16) : kNowhere;
     }
   }
+  template <bool ONCE>
   static __device__ __forceinline__ void load(const Group &g, int lane, const uint32_t (&off)[kLoads], FB_LDS int8_t *dst) {
     const __amdgpu_buffer_rsrc_t from = buffer_of(g.base, g.bytes);
 #pragma unroll
     for (int i = 0; i < kLoads; ++i) {
       const int row = i * kRows + lane / (D / 8);
-      load_to_lds(from, g.first > 0 && row < g.first ? kNowhere : off[i], 0, dst + i * 1024);
+      load_to_lds<ONCE>(from, g.first > 0 && row < g.first ? kNowhere : off[i], 0, dst + i * 1024);
     }
   }
 };
@@ -221,8 +222,10 @@ struct WaveTile {
     }
   }
 
-  // S^T of the tile.
-  __device__ __forceinline__ void scores(const int8_t *kt, int lane, f32x16 (&s)[KB][QB]) const {
+  typedef f32x16 Scores[KB][QB];  // S^T of a tile
+  typedef u32x4 Weights[KB][2][QB];
+
+  __device__ __forceinline__ void scores(const int8_t *kt, int lane, Scores &s) const {
 #pragma unroll
     for (int k = 0; k < KB; ++k) {
 #pragma unroll
@@ -238,7 +241,7 @@ struct WaveTile {
   }
 
   // Scores to weights, with what that does to m, l and o.
-  __device__ __forceinline__ void weights(float c, f32x16 (&s)[KB][QB], u32x4 (&w)[KB][2][QB]) {
+  __device__ __forceinline__ void weights(float c, Scores &s, Weights &w) {
     float top[QB];
     bool rise = false;
 #pragma unroll
@@ -282,7 +285,7 @@ struct WaveTile {
     }
   }
 
-  __device__ __forceinline__ void add_values(const int8_t *vt, int lane, const u32x4 (&w)[KB][2][QB]) {
+  __device__ __forceinline__ void add_values(const int8_t *vt, int lane, const Weights &w) {
 #pragma unroll
     for (int k = 0; k < KB; ++k)
 #pragma unroll
@@ -295,14 +298,11 @@ struct WaveTile {
         }
   }
 
-  // The tile that begins at key0.  part: the border of a row's view lies in it, or
-  // keys that are not there (bit g of `there`: its group g of 16 has a page).
-  // (The empty asm makes a value of the rare work known there only, which keeps the
-  // compiler from doing that work always.)
-  __device__ __forceinline__ void take(float c, const int8_t *kt, const int8_t *vt, bool part, int key0, uint32_t there, int lane) {
-    f32x16 s[KB][QB];
-    u32x4 w[KB][2][QB];
-    scores(kt, lane, s);
+  // Leaves out what a row does not see of the tile that begins at key0.  part: the
+  // border of a row's view lies in it, or keys that are not there (bit g of `there`:
+  // its group g of 16 has a page).  (The empty asm makes a value of the rare work
+  // known there only, which keeps the compiler from doing that work always.)
+  __device__ __forceinline__ void mask(Scores &s, bool part, int key0, uint32_t there, int lane) const {
     if (part) {
       int mine = key0 + 4 * (lane / 32);
       asm volatile("" : "+v"(mine));
@@ -317,8 +317,6 @@ struct WaveTile {
             s[k][x][i] = seen ? s[k][x][i] : -__builtin_inff();
           }
     }
-    weights(c, s, w);
-    add_values(vt, lane, w);
   }
 
   // V^T of dimensions 32 i .. + 31 and 16 keys in the order of the weights: lane l
@@ -448,7 +446,8 @@ __global__ __launch_bounds__(256, 2) void attention_chunk_kernel(const Attention
 
   const int begin = r.lo / KT, all = max(0, (r.hi + KT - 1) / KT - begin), per = (all + a.splits - 1) / a.splits;
   const int t0 = begin + min(split * per, all), t1 = begin + min((split + 1) * per, all);
-  WaveTile<E, D, QB, KT> w;
+  typedef WaveTile<E, D, QB, KT> Tile;
+  Tile w;
   w.start(a, r, head, wave * 32 * QB, lane);
 
   uint32_t off[JOBS][Loads::kLoads];
@@ -473,7 +472,7 @@ __global__ __launch_bounds__(256, 2) void attention_chunk_kernel(const Attention
     for (int j = 0; j < JOBS; ++j) {
       const int job = j * 4 + wave, g = job % GROUPS;
       const bool value = job / GROUPS;
-      Loads::load(group_of(b, value ? b.v : b.k, head, t * KT + 16 * g, __builtin_amdgcn_readlane(pages, g), r), lane, off[j],
+      Loads::template load<false>(group_of(b, value ? b.v : b.k, head, t * KT + 16 * g, __builtin_amdgcn_readlane(pages, g), r), lane, off[j],
                   (FB_LDS int8_t *)lds[buf][value] + g * 16 * D * 2);
     }
   };
@@ -494,7 +493,12 @@ __global__ __launch_bounds__(256, 2) void attention_chunk_kernel(const Attention
     find_pages(t + 2);
     const bool border = key0 + KT - 1 > r.p_lo || (a.window && key0 <= r.p_hi - a.window);
     if (border && r.p_lo != r.p_hi) bad = bad || w.unclean(lds[buf][1], lane);
-    w.take(a.c, lds[buf][0], lds[buf][1], border || now != (1u << GROUPS) - 1 || key0 + KT > r.hi, key0, now, lane);
+    typename Tile::Scores s;
+    typename Tile::Weights p;
+    w.scores(lds[buf][0], lane, s);
+    w.mask(s, border || now != (1u << GROUPS) - 1 || key0 + KT > r.hi, key0, now, lane);
+    w.weights(a.c, s, p);
+    w.add_values(lds[buf][1], lane, p);
   }
   if (bad) {
     rows_one_by_one<E>(a, r, head, split, first_row, end_row, 1, t0 * KT, t1 * KT, lane);
@@ -517,20 +521,24 @@ __global__ __launch_bounds__(256, 2) void attention_chunk_kernel(const Attention
   }
 }
 
-// Up to 32 rows: the waves share them and split the keys, each with a ring of
-// tiles of its own, so that nothing waits for another wave before the end.
+// Up to 32 rows: the waves share them and split the keys, each with a place of its
+// own for a tile's keys and one for its values, loaded again as soon as they have
+// been read, so that nothing waits for another wave before the end and a wave
+// always has loads in flight.  Keys and values are read once and marked so (64
+// sequences of up to 8192 keys: 163 us for 181).  Eight waves of 16 KiB: a wave's chain of products and
+// weights is long for a single query, and two to a SIMD hide it better than more
+// tiles ahead of fewer waves.
 template <int D>
 struct Few {
-  static constexpr int W = D == 256 ? 2 : 4, STAGES = 2, KT = 32, BYTES = KT * D * 2;
+  static constexpr int W = D == 256 ? 4 : 8, KT = 32, BYTES = KT * D * 2;
 };
 template <typename E, int D>
 __global__ __launch_bounds__(64 * Few<D>::W) void attention_few_kernel(const AttentionArgs a) {
   typedef Few<D> F;
-  constexpr int W = F::W, S = F::STAGES, KT = F::KT, BYTES = F::BYTES;
+  constexpr int W = F::W, KT = F::KT, BYTES = F::BYTES;
   typedef GroupLoads<D> Loads;
-  constexpr int ROW = D + 4;  // floats of a row of the joined sums: rows four banks apart
-  static_assert(W * 32 * ROW * 4 <= W * S * 2 * BYTES, "the waves' sums take the place of the tiles");
-  __shared__ __align__(1024) int8_t lds[W * S * 2 * BYTES];
+  typedef WaveTile<E, D, 1, KT> Tile;
+  __shared__ __align__(1024) int8_t lds[W * 2 * BYTES];  // the waves' sums, 32 x D floats each, take it over
   __shared__ float stats[2][W][32];
   __shared__ bool any_bad[W];
   const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
@@ -542,54 +550,53 @@ __global__ __launch_bounds__(64 * Few<D>::W) void attention_few_kernel(const Att
 
   const int begin = r.lo / KT, all = max(0, (r.hi + KT - 1) / KT - begin), per = (all + a.splits - 1) / a.splits;
   const int t0 = begin + min(split * per, all), t1 = begin + min((split + 1) * per, all);
-  WaveTile<E, D, 1, KT> w;
+  Tile w;
   w.start(a, r, head, 0, lane);
 
   uint32_t off_k[Loads::kLoads], off_v[Loads::kLoads];
   Loads::offsets(b, lane, false, off_k);
   Loads::offsets(b, lane, true, off_v);
-  int8_t *mine = lds + wave * S * 2 * BYTES;
+  int8_t *const kt = lds + wave * 2 * BYTES, *const vt = kt + BYTES;
   // lane 2 i + g of `pages`: the page of the group g of the wave's tile number i
   // after the last look-up, made every 32 tiles
   int pages = -1;
-  uint32_t there[S];
+  const auto page = [&](int n, int g) { return __builtin_amdgcn_readlane(pages, n % 32 * 2 + g); };
   // The wave's tile number n.  Loads of tiles that do not exist read an empty
-  // buffer, so that every stage counts the same number of loads.
-  const auto fetch = [&](int n, int stage) {
+  // buffer, so that every tile counts the same number of loads.
+  const auto fetch = [&](int n, const uint16_t *cache, const uint32_t (&off)[Loads::kLoads], int8_t *dst) {
+#pragma unroll
+    for (int g = 0; g < 2; ++g)
+      Loads::template load<true>(group_of(b, cache, head, (t0 + wave + n * W) * KT + 16 * g, page(n, g), r), lane, off, (FB_LDS int8_t *)dst + g * 16 * D * 2);
+  };
+  const auto find_pages = [&](int n) {
     if (n % 32 == 0) {
       const int t = t0 + wave + (n + lane / 2) * W;
       pages = t < t1 ? page_of(b, r.seq, t * KT + 16 * (lane % 2)) : -1;
     }
-    const int t = t0 + wave + n * W;
-    int8_t *dst = mine + stage * 2 * BYTES;
-    there[stage] = 0;
-#pragma unroll
-    for (int g = 0; g < 2; ++g) {
-      const int page = __builtin_amdgcn_readlane(pages, n % 32 * 2 + g);
-      there[stage] |= (uint32_t)(page >= 0) << g;
-      Loads::load(group_of(b, b.k, head, t * KT + 16 * g, page, r), lane, off_k, (FB_LDS int8_t *)dst + g * 16 * D * 2);
-      Loads::load(group_of(b, b.v, head, t * KT + 16 * g, page, r), lane, off_v, (FB_LDS int8_t *)dst + BYTES + g * 16 * D * 2);
-    }
   };
   bool bad = false;
-  const auto work = [&](int t, int stage) {
-    const int key0 = t * KT;
-    const int8_t *from = mine + stage * 2 * BYTES;
+  find_pages(0);
+  fetch(0, b.k, off_k, kt);
+  fetch(0, b.v, off_v, vt);
+#pragma unroll 1
+  for (int n = 0; t0 + wave + n * W < t1; ++n) {
+    const int key0 = (t0 + wave + n * W) * KT;
     const bool border = key0 + KT - 1 > r.p_lo || (a.window && key0 <= r.p_hi - a.window);
-    if (border && r.p_lo != r.p_hi) bad = bad || w.unclean(from + BYTES, lane);
-    w.take(a.c, from, from + BYTES, border || there[stage] != 3 || key0 + KT > r.hi, key0, there[stage], lane);
-  };
-#pragma unroll
-  for (int i = 0; i < S; ++i) fetch(i, i);
-  for (int n = 0; t0 + wave + n * W < t1; n += S) {
-#pragma unroll
-    for (int i = 0; i < S; ++i) {
-      wait_for_loads<(S - 1) * 4 * Loads::kLoads>();
-      const int t = t0 + wave + (n + i) * W;
-      if (t < t1) work(t, i);
-      wait_for_reads();
-      fetch(n + S + i, i);
-    }
+    const uint32_t there = (page(n, 0) >= 0) | (page(n, 1) >= 0) << 1;
+    typename Tile::Scores s;
+    typename Tile::Weights p;
+    find_pages(n + 1);
+    wait_for_loads<2 * Loads::kLoads>();
+    w.scores(kt, lane, s);
+    wait_for_reads();
+    fetch(n + 1, b.k, off_k, kt);
+    w.mask(s, border || there != 3 || key0 + KT > r.hi, key0, there, lane);
+    w.weights(a.c, s, p);
+    wait_for_loads<2 * Loads::kLoads>();
+    if (border && r.p_lo != r.p_hi) bad = bad || w.unclean(vt, lane);
+    w.add_values(vt, lane, p);
+    wait_for_reads();
+    fetch(n + 1, b.v, off_v, vt);
   }
 
   // Join the waves.
@@ -613,12 +620,15 @@ __global__ __launch_bounds__(64 * Few<D>::W) void attention_few_kernel(const Att
 #pragma unroll
   for (int v = 0; v < W; ++v) top = fmaxf(top, stats[0][v][mine_row]);
   const float factor = w.m[0] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f((w.m[0] - top) * a.c);
+  // four floats to a place, places exchanged by the row so that rows fall into
+  // different banks
   float *sums = reinterpret_cast<float *>(lds);
+  const auto sum_at = [](int row, int place) { return (place ^ row % 16) * 4; };
 #pragma unroll
   for (int i = 0; i < D / 32; ++i)
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-      *reinterpret_cast<f32x4 *>(sums + (wave * 32 + mine_row) * ROW + 32 * i + 8 * j + 4 * (lane / 32)) =
+      *reinterpret_cast<f32x4 *>(sums + (wave * 32 + mine_row) * D + sum_at(mine_row, 8 * i + 2 * j + lane / 32)) =
           f32x4{w.o[i][0][4 * j], w.o[i][0][4 * j + 1], w.o[i][0][4 * j + 2], w.o[i][0][4 * j + 3]} * factor;
   __syncthreads();
   for (int x = threadIdx.x; x < rows * (D / 4); x += 64 * W) {
@@ -633,7 +643,7 @@ __global__ __launch_bounds__(64 * Few<D>::W) void attention_few_kernel(const Att
       const float m = stats[0][v][row];
       if (m == -__builtin_inff()) continue;
       sum = fmaf(stats[1][v][row], __builtin_amdgcn_exp2f((m - big) * a.c), sum);
-      o += *reinterpret_cast<const f32x4 *>(sums + (v * 32 + row) * ROW + d);
+      o += *reinterpret_cast<const f32x4 *>(sums + (v * 32 + row) * D + sum_at(row, d / 4));
     }
     place_of(a, r, head, r.first + row, split, big * a.c, sum, d == 0).put<E>(d, o);
   }
@@ -656,10 +666,21 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttentionArgs
   const float top = wave_reduce<MaxF>(cm);
   const float f = cm == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(cm - top);
   const float sum = wave_reduce<SumF>(f == 0.0f ? 0.0f : f * l);
+  // eight splits' parts are in flight; parts of splits without keys may hold anything
   f32x4 o{0, 0, 0, 0};
-  for (int s = 0; s < a.splits; ++s) {
-    const float fs = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), s));
-    if (fs != 0.0f && 4 * lane < b.dim) o += *reinterpret_cast<const f32x4 *>(a.part + (row * a.splits + s) * b.dim + 4 * lane) * fs;
+  const float *part = a.part + row * a.splits * b.dim + 4 * lane;
+  for (int base = 0; base < a.splits; base += 8) {
+    f32x4 v[8];
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      v[i] = f32x4{0, 0, 0, 0};
+      if (base + i < a.splits && 4 * lane < b.dim) v[i] = *reinterpret_cast<const f32x4 *>(part + (base + i) * b.dim);
+    }
+#pragma unroll
+    for (int i = 0; i < 8; ++i) {
+      const float fs = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), (base + i) % 64));
+      if (base + i < a.splits && fs != 0.0f) o += v[i] * fs;
+    }
   }
   const Place place{a.out + (int64_t)token * a.ldo + row % b.heads * b.dim, nullptr, sum == 0.0f ? 0.0f : 1.0f / sum};
   if (4 * lane < b.dim) place.put<E>(4 * lane, o);

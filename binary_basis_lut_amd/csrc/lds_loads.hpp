@@ -24,9 +24,11 @@ __device__ __forceinline__ __amdgpu_buffer_rsrc_t buffer_of(const int8_t *base, 
 // Sixteen bytes per lane from global memory straight into LDS: lane l's piece, at
 // base + soff + voff, lands at dst + 16 l.  A buffer load rather than a global
 // one: the compiler takes a direct global load for an LDS access too and would
-// then wait for all fragment reads in flight wherever it waits for some.
+// then wait for all fragment reads in flight wherever it waits for some.  ONCE: of
+// data that nobody reads again, which then does not push other data out of the L2.
+template <bool ONCE = false>
 __device__ __forceinline__ void load_to_lds(__amdgpu_buffer_rsrc_t base, uint32_t voff, uint32_t soff, FB_LDS int8_t *dst) {
-  __builtin_amdgcn_raw_ptr_buffer_load_lds(base, (FB_LDS void *)dst, 16, voff, soff, 0, 0);
+  __builtin_amdgcn_raw_ptr_buffer_load_lds(base, (FB_LDS void *)dst, 16, voff, soff, 0, ONCE ? 2 : 0);
 }
 
 // Waits until at most `vm` of the wave's vector-memory operations and none of

@@ -8,8 +8,8 @@ using namespace fluxbin;
 
 namespace {
 
-constexpr int64_t kTargetGroups = 512;  // two to a CU
-constexpr int64_t kMinKeys = 256;       // of a split
+constexpr int64_t kTargetGroups = 256;  // one to a CU
+constexpr int64_t kMinKeys = 512;       // of a split
 constexpr int64_t kMaxSplits = 64;      // the join's lanes
 constexpr int64_t kMaxGrid = ((int64_t)1 << 24) - 1;
 
