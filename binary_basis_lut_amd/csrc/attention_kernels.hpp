@@ -46,9 +46,10 @@ struct AttentionArgs {
   const uint16_t *q;
   uint16_t *out;
   float *lse;      // may be null
-  float *part;     // splits > 1: o of [row][split][dim], then (c m, l) of [row][split]
-  int64_t ldq, ldo, parts;  // parts: tokens * heads * splits
-  int32_t group, window, splits, tiles;
+  float *part, *stats;  // parts of rows: o [part][dim], (c m, l) [part]
+  int32_t *before;      // balanced: key tiles of the row tiles before each, and of all of them
+  int64_t ldq, ldo;
+  int32_t group, window, splits, tiles, workgroups;
   float c;
 };
 
@@ -121,27 +122,36 @@ struct Rows {
   int lo, hi;                // keys that some row sees, [lo, hi)
 };
 
+// Tile numbers of sequence s start at floor(start * G / BM) + s, which leaves every
+// sequence at least the tiles that its rows fill.  Starts are cut to the rows that
+// exist.
 template <int BM>
-__device__ __forceinline__ Rows rows_of(const AttentionArgs &a, int tile, int lane) {
+__device__ __forceinline__ int first_tile(const AttentionArgs &a, int start, int s) {
+  return (int)((int64_t)max(0, min(start, a.b.tokens)) * a.group / BM) + s;
+}
+
+template <int BM>
+__device__ __forceinline__ Rows rows_at(const AttentionArgs &a, int tile, const Found &f) {
   const Paged &b = a.b;
   Rows r{};
-  // Tile numbers of sequence s start at floor(start * G / BM) + s, which leaves
-  // every sequence at least the tiles that its rows fill.
-  const auto first_tile = [&](int s) { return (int)((int64_t)row_start(b, s) * a.group / BM) + s; };
-  r.seq = count_starts(b.seqs, lane, [&](int s) { return first_tile(s) <= tile; });
+  r.seq = f.seq;
   if (r.seq >= b.seqs) return r;
-  r.start = row_start(b, r.seq);
-  const int n = row_start(b, r.seq + 1) - r.start;
-  r.first = (tile - first_tile(r.seq)) * BM;
+  r.start = max(0, min(f.start, b.tokens));
+  const int n = max(0, min(f.next, b.tokens)) - r.start;
+  r.first = (tile - first_tile<BM>(a, f.start, r.seq)) * BM;
   if (n <= 0 || r.first < 0 || r.first >= n * a.group) return r;
   r.count = n * a.group;
-  const int len = b.kv_lens[r.seq], given = b.seq_starts ? b.seq_starts[r.seq + 1] - b.seq_starts[r.seq] : 1;
-  r.before = len - given + (b.seq_starts ? r.start - b.seq_starts[r.seq] : 0);
+  r.before = f.len - (f.next - f.start) + (r.start - f.start);
   r.p_lo = r.before + r.first / a.group;
   r.p_hi = r.before + (min(r.first + BM, r.count) - 1) / a.group;
   r.hi = max(0, min(r.p_hi, (b.table_pages << b.page_shift) - 1) + 1);
-  r.lo = a.window ? max(0, r.p_lo - a.window + 1) : 0;
+  r.lo = min(r.hi, a.window ? max(0, r.p_lo - a.window + 1) : 0);
   return r;
+}
+
+template <int BM>
+__device__ __forceinline__ Rows rows_of(const AttentionArgs &a, int tile, int lane) {
+  return rows_at<BM>(a, tile, find_sequence(a.b, lane, [&](int start, int s) { return first_tile<BM>(a, start, s) <= tile; }));
 }
 
 // One group of 16 keys on its way to LDS: where it comes from and which of its
@@ -364,22 +374,30 @@ struct Place {
   }
 };
 
-// Where a row's o goes; its lse, or the split's (c m, l), is written here by the
-// lane that is `first` of those that have the row.
-__device__ __forceinline__ Place place_of(const AttentionArgs &a, const Rows &r, int head, int row, int split, float cm, float l, bool first) {
-  const int64_t at = (int64_t)(r.start + row / a.group) * a.b.heads + head * a.group + row % a.group;
+// Where a row's o goes: the output, or its part number `index` (< 0: none).  The
+// row's lse, or the part's (c m, l), is written here by the lane that is `first` of
+// those that have the row.
+__device__ __forceinline__ Place place_of(const AttentionArgs &a, const Rows &r, int head, int row, int64_t index, float cm, float l, bool first) {
+  const int token = r.start + row / a.group, h = head * a.group + row % a.group;
   Place p;
-  p.out = a.out + (int64_t)(r.start + row / a.group) * a.ldo + (head * a.group + row % a.group) * a.b.dim;
-  p.part = a.splits > 1 ? a.part + (at * a.splits + split) * a.b.dim : nullptr;
+  p.out = a.out + (int64_t)token * a.ldo + h * a.b.dim;
+  p.part = index >= 0 ? a.part + index * a.b.dim : nullptr;
   p.inv = l == 0.0f ? 0.0f : 1.0f / l;
-  if (first && a.splits > 1) {
-    a.part[a.parts * a.b.dim + 2 * (at * a.splits + split)] = cm;
-    a.part[a.parts * a.b.dim + 2 * (at * a.splits + split) + 1] = l;
+  if (first && index >= 0) {
+    a.stats[2 * index] = cm;
+    a.stats[2 * index + 1] = l;
   } else if (first && a.lse) {
-    a.lse[at] = lse_of(cm, l);
+    a.lse[(int64_t)token * a.b.heads + h] = lse_of(cm, l);
   }
   return p;
 }
+
+// Which parts the rows of a workgroup write: row x of them is part `from` + x `step`
+// (from < 0: none, the rows are whole).
+struct Parts {
+  int64_t from, step;
+  __device__ __forceinline__ int64_t of(int x) const { return from < 0 ? -1 : from + x * step; }
+};
 
 // Rows [from, to) of a workgroup over the keys [k0, k1), one after the other by a
 // wave: 64 keys at a time, a lane to a key, then a lane to four dimensions.  For
@@ -387,8 +405,8 @@ __device__ __forceinline__ Place place_of(const AttentionArgs &a, const Rows &r,
 // matrix product would carry to all of them (0 times infinity): here a key whose
 // weight is 0 is left out.
 template <typename E>
-__device__ __forceinline__ void rows_one_by_one(const AttentionArgs &a, const Rows &r, int head, int split, int from, int to, int step, int k0,
-                                         int k1, int lane) {
+__device__ __forceinline__ void rows_one_by_one(const AttentionArgs &a, const Rows &r, int head, const Parts &parts, int from, int to, int step,
+                                                int k0, int k1, int lane) {
   const Paged &b = a.b;
   for (int row = from; row < to; row += step) {
     const int token = row / a.group, p = r.before + token, first = a.window ? max(0, p - a.window + 1) : 0;
@@ -422,86 +440,85 @@ __device__ __forceinline__ void rows_one_by_one(const AttentionArgs &a, const Ro
           for (int i = 0; i < 4; ++i) o[i] = fmaf(wj, E::load(b.v[v + 4 * lane + i]), o[i]);
       }
     }
-    const Place place = place_of(a, r, head, row, split, m * a.c, l, lane == 0);
+    const Place place = place_of(a, r, head, row, parts.of(row - r.first), m * a.c, l, lane == 0);
     if (4 * lane < b.dim) place.put<E>(4 * lane, o);
   }
 }
 
-// 128 x QB rows, 32 x QB to each of four waves, over one split of their keys; a
-// workgroup's tiles of KT keys come by two buffers, the next one loaded while one is
-// worked on.
-template <typename E, int D, int QB>
-__global__ __launch_bounds__(256, 2) void attention_chunk_kernel(const AttentionArgs a) {
-  constexpr int BM = 128 * QB, KT = D == 256 ? 32 : 64, GROUPS = KT / 16, JOBS = 2 * GROUPS / 4, BYTES = KT * D * 2;
-  typedef GroupLoads<D> Loads;
-  __shared__ __align__(1024) int8_t lds[2][2][BYTES];  // [buffer][K, V]
-  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
-  const Paged &b = a.b;
-  // key heads go to the XCDs in turn, so that the workgroups that share one's
-  // keys share an L2; the last tiles, which see most, start first
-  const int head = blockIdx.x % b.kv_heads, rest = blockIdx.x / b.kv_heads;
-  const int split = rest % a.splits, tile = a.tiles - 1 - rest / a.splits;
-  const Rows r = rows_of<BM>(a, tile, lane);
-  if (r.count == 0) return;
+constexpr int kChunkKeys = 64;  // keys of a tile: a group of 16 to each of four waves
 
-  const int begin = r.lo / KT, all = max(0, (r.hi + KT - 1) / KT - begin), per = (all + a.splits - 1) / a.splits;
-  const int t0 = begin + min(split * per, all), t1 = begin + min((split + 1) * per, all);
+// What a workgroup of 128 x QB rows keeps in LDS: two buffers of a tile's keys and
+// values.
+template <int D>
+struct ChunkTiles {
+  static constexpr int KT = kChunkKeys, BYTES = KT * D * 2;
+  int8_t tile[2][2][BYTES];
+};
+
+// 128 x QB rows, 32 x QB to each of four waves, over the key tiles [t0, t1), from
+// t0 + turn on and round to it again; they come by two buffers, the next one loaded
+// while one is worked on.
+template <typename E, int D, int QB>
+__device__ __forceinline__ void attend_rows(const AttentionArgs &a, const Rows &r, int head, int t0, int t1, int turn,
+                                            const Parts &parts, ChunkTiles<D> &lds, int lane, int wave) {
+  constexpr int KT = kChunkKeys, GROUPS = KT / 16;
+  typedef GroupLoads<D> Loads;
+  const Paged &b = a.b;
   typedef WaveTile<E, D, QB, KT> Tile;
   Tile w;
   w.start(a, r, head, wave * 32 * QB, lane);
 
-  uint32_t off[JOBS][Loads::kLoads];
-#pragma unroll
-  for (int j = 0; j < JOBS; ++j) Loads::offsets(b, lane, (j * 4 + wave) / GROUPS, off[j]);
+  uint32_t off_k[Loads::kLoads], off_v[Loads::kLoads];
+  Loads::offsets(b, lane, false, off_k);
+  Loads::offsets(b, lane, true, off_v);
   // lane i: the page of group i of the tile that is fetched next.  The number is looked
   // at a tile later than it is asked for (the asm keeps the compiler from looking at
   // once), since a wait for it is a wait for all loads before it.
   int pages;
-  const auto find_pages = [&](int t) {
-    const int i = (t * KT + 16 * (lane % GROUPS)) >> b.page_shift;
+  const int tiles = t1 - t0;
+  const auto tile_at = [&](int n) { return t0 + n + turn < t1 ? t0 + n + turn : n + turn - tiles + t0; };
+  const auto find_pages = [&](int n) {
+    const int i = (tile_at(n) * KT + 16 * (lane % GROUPS)) >> b.page_shift;
     pages = -1;
-    if (t < t1 && i < b.table_pages) pages = b.page_table[(int64_t)r.seq * b.table_ld + i];
+    if (n < tiles && i < b.table_pages) pages = b.page_table[(int64_t)r.seq * b.table_ld + i];
   };
   const auto settle = [&]() {
     asm volatile("" : "+v"(pages));
     pages = (uint32_t)pages < (uint32_t)b.pages ? pages : -1;
   };
   const auto there_of = [&]() { return (uint32_t)__ballot(pages >= 0) & ((1u << GROUPS) - 1); };
-  const auto fetch = [&](int t, int buf) {
-#pragma unroll
-    for (int j = 0; j < JOBS; ++j) {
-      const int job = j * 4 + wave, g = job % GROUPS;
-      const bool value = job / GROUPS;
-      Loads::template load<false>(group_of(b, value ? b.v : b.k, head, t * KT + 16 * g, __builtin_amdgcn_readlane(pages, g), r), lane, off[j],
-                  (FB_LDS int8_t *)lds[buf][value] + g * 16 * D * 2);
-    }
+  const auto fetch = [&](int n) {  // a wave fetches a group's keys and values
+    const int key0 = tile_at(n) * KT + 16 * wave, page = __builtin_amdgcn_readlane(pages, wave);
+    FB_LDS int8_t *const k = (FB_LDS int8_t *)lds.tile[n % 2][0] + wave * 16 * D * 2, *const v = (FB_LDS int8_t *)lds.tile[n % 2][1] + wave * 16 * D * 2;
+    Loads::template load<false>(group_of(b, b.k, head, key0, page, r), lane, off_k, k);
+    Loads::template load<false>(group_of(b, b.v, head, key0, page, r), lane, off_v, v);
   };
-  find_pages(t0);
+  find_pages(0);
   settle();
   uint32_t there = there_of();
-  if (t0 < t1) fetch(t0, 0);
-  find_pages(t0 + 1);
+  if (tiles > 0) fetch(0);
+  find_pages(1);
   const int first_row = r.first + wave * 32 * QB, end_row = min(first_row + 32 * QB, r.count);
   bool bad = false;
-  for (int t = t0; t < t1; ++t) {
-    const int buf = (t - t0) % 2, key0 = t * KT;
+  for (int n = 0; n < tiles; ++n) {
+    const int buf = n % 2, key0 = tile_at(n) * KT;
     wait_and_meet<0>();
     const uint32_t now = there;
     settle();
     there = there_of();
-    if (t + 1 < t1) fetch(t + 1, buf ^ 1);
-    find_pages(t + 2);
+    if (n + 1 < tiles) fetch(n + 1);
+    find_pages(n + 2);
     const bool border = key0 + KT - 1 > r.p_lo || (a.window && key0 <= r.p_hi - a.window);
-    if (border && r.p_lo != r.p_hi) bad = bad || w.unclean(lds[buf][1], lane);
+    if (border && r.p_lo != r.p_hi) bad = bad || w.unclean(lds.tile[buf][1], lane);
     typename Tile::Scores s;
     typename Tile::Weights p;
-    w.scores(lds[buf][0], lane, s);
+    w.scores(lds.tile[buf][0], lane, s);
     w.mask(s, border || now != (1u << GROUPS) - 1 || key0 + KT > r.hi, key0, now, lane);
     w.weights(a.c, s, p);
-    w.add_values(lds[buf][1], lane, p);
+    w.add_values(lds.tile[buf][1], lane, p);
   }
   if (bad) {
-    rows_one_by_one<E>(a, r, head, split, first_row, end_row, 1, t0 * KT, t1 * KT, lane);
+    rows_one_by_one<E>(a, r, head, parts, first_row, end_row, 1, t0 * KT, t1 * KT, lane);
     return;
   }
 #pragma unroll
@@ -509,7 +526,7 @@ __global__ __launch_bounds__(256, 2) void attention_chunk_kernel(const Attention
     const int row = first_row + 32 * x + lane % 32;
     const float l = other_half_sum(w.l[x]);
     if (row >= end_row) continue;
-    const Place place = place_of(a, r, head, row, split, w.m[x] * a.c, l, lane < 32);
+    const Place place = place_of(a, r, head, row, parts.of(row - r.first), w.m[x] * a.c, l, lane < 32);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -519,6 +536,163 @@ __global__ __launch_bounds__(256, 2) void attention_chunk_kernel(const Attention
           place.put<E>(d, f32x4{w.o[i][x][4 * j], w.o[i][x][4 * j + 1], w.o[i][x][4 * j + 2], w.o[i][x][4 * j + 3]});
       }
   }
+}
+
+// Workgroups that a CU holds: with 256 dimensions the registers of a wave and the
+// LDS are enough for one (two of 32-key tiles spill, and run at 690 TFLOP/s for 824).
+template <int D>
+constexpr int kChunksPerCu = D == 256 ? 1 : 2;
+
+// One row tile and key head to a workgroup.
+template <typename E, int D, int QB>
+__global__ __launch_bounds__(256, kChunksPerCu<D>) void attention_chunk_kernel(const AttentionArgs a) {
+  constexpr int KT = kChunkKeys;
+  __shared__ __align__(1024) ChunkTiles<D> lds;
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  // key heads go to the XCDs in turn, so that the workgroups that share one's
+  // keys share an L2; the last tiles, which see most, start first
+  const int head = blockIdx.x % a.b.kv_heads, tile = a.tiles - 1 - blockIdx.x / a.b.kv_heads;
+  const Rows r = rows_of<128 * QB>(a, tile, lane);
+  if (r.count == 0) return;
+  attend_rows<E, D, QB>(a, r, head, r.lo / KT, (r.hi + KT - 1) / KT, 0, Parts{-1, 0}, lds, lane, wave);
+}
+
+// Where there are few row tiles: the key tiles of all row tiles and heads, one behind
+// the other, divided into equal shares, one to a workgroup.  A share is shorter than
+// most row tiles' keys, so it is a run of one of them, or the end of one and the
+// beginning of the next.  A workgroup has at most two parts for the join: number 2 g
+// of a row tile that it goes on with and 2 g + 1 of one that it begins and does not
+// end.
+//
+// The number of key tiles before each row tile; a row tile without keys counts as
+// one, so that its rows are written.  A thread to a tile, kTilesMost of them.
+constexpr int kTilesMost = 4096;
+template <int BM>
+__global__ __launch_bounds__(1024) void attention_count_kernel(const AttentionArgs a) {
+  constexpr int KT = kChunkKeys;
+  __shared__ int sums[16];
+  const Paged &b = a.b;
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  int total = 0;
+  for (int base = 0; base < a.tiles; base += 1024) {
+    const int tile = base + (int)threadIdx.x;
+    int n = 0;
+    if (tile < a.tiles) {
+      // the sequence: the last one whose tiles begin at or before this one
+      int lo = 0, hi = b.seqs;
+      while (lo < hi) {
+        const int mid = (lo + hi + 1) / 2, start = b.seq_starts ? max(0, min(b.seq_starts[mid], b.tokens)) : mid;
+        if ((int)((int64_t)start * a.group / BM) + mid <= tile) lo = mid;
+        else hi = mid - 1;
+      }
+      if (lo < b.seqs) {
+        const int start = b.seq_starts ? b.seq_starts[lo] : lo, next = b.seq_starts ? b.seq_starts[lo + 1] : lo + 1;
+        const Rows r = rows_at<BM>(a, tile, Found{lo, start, next, b.kv_lens[lo]});
+        if (r.count) n = max(1, (r.hi + KT - 1) / KT - r.lo / KT);
+      }
+    }
+    int sum = n;  // of the lanes up to this one
+    for (int d = 1; d < 64; d *= 2) {
+      const int v = __shfl_up(sum, d);
+      if (lane >= d) sum += v;
+    }
+    if (lane == 63) sums[wave] = sum;
+    __syncthreads();
+    int ahead = total;
+    for (int w = 0; w < 16; ++w) {
+      if (w < wave) ahead += sums[w];
+      total += sums[w];
+    }
+    if (tile < a.tiles) a.before[tile] = ahead + sum - n;
+    __syncthreads();
+  }
+  if (threadIdx.x == 0) a.before[a.tiles] = total;
+}
+
+// Key tiles to a workgroup: equal shares, but none so small that its parts are most
+// of its work.  (The host has seen to it that all key tiles are below 2^31.)
+constexpr int kLeastShare = 8;
+__device__ __forceinline__ int share_of(const AttentionArgs &a, int all) { return max(kLeastShare, (all + a.workgroups - 1) / a.workgroups); }
+
+// The tile that has key tile `in` of a head: the last one that begins at or before
+// it (tiles without rows, which take no room, begin with the next one).
+__device__ __forceinline__ int tile_with(const AttentionArgs &a, int in, int lane) {
+  int tile = 0, n = a.tiles - 1;
+  while (n > 0) {
+    const int step = (n + 63) / 64, j = (lane + 1) * step;
+    const int c = __popcll(__ballot(j <= n && a.before[tile + j] <= in));
+    tile += c * step;
+    n = min(step - 1, n - c * step);
+  }
+  return tile;
+}
+
+template <typename E, int D, int QB>
+__global__ __launch_bounds__(256, kChunksPerCu<D>) void attention_balanced_kernel(const AttentionArgs a) {
+  constexpr int KT = kChunkKeys, BM = 128 * QB;
+  __shared__ __align__(1024) ChunkTiles<D> lds;
+  const int lane = threadIdx.x % 64, wave = __builtin_amdgcn_readfirstlane(threadIdx.x / 64);
+  // an XCD's workgroups have consecutive shares: the same head's, mostly
+  const int g = blockIdx.x % 8 * (a.workgroups / 8) + blockIdx.x / 8;
+  const int per_head = a.before[a.tiles], all = per_head * a.b.kv_heads, share = share_of(a, all);
+  const int first = (int)min((int64_t)g * share, (int64_t)all);
+  // Workgroups that share a head's keys should read the same ones at about the same
+  // time, so that one of them finds what another has loaded in the L2: a share's key
+  // tiles are taken in the order of their number modulo the share's length.  So the
+  // beginning of the next row tile goes before the end of the last one, and a run
+  // starts at the multiple of the length that lies in it.
+  int end = (int)min((int64_t)first + share, (int64_t)all);
+#pragma unroll 1
+  while (end > first) {
+    const int head = (end - 1) / per_head, in = (end - 1) % per_head;
+    const int tile = tile_with(a, in, lane), before = a.before[tile], size = a.before[tile + 1] - before;
+    const int to = in + 1 - before, from = max(0, to - (end - first));
+    const Rows r = rows_of<BM>(a, tile, lane);
+    const int begin = r.lo / KT, last = (r.hi + KT - 1) / KT, whole = (from + share - 1) / share * share;
+    __syncthreads();  // the tiles of the last rows have been read
+    attend_rows<E, D, QB>(a, r, head, begin + from, min(begin + to, last), whole < min(to, last - begin) ? whole - from : 0,
+                          from == 0 && to == size ? Parts{-1, 0} : Parts{((int64_t)2 * g + (from == 0)) * BM, 1}, lds, lane, wave);
+    end -= to - from;
+  }
+}
+
+// The parts of the row tiles that several workgroups had, joined; a row to a wave.
+template <typename E, int BM>
+__global__ __launch_bounds__(256) void attention_gather_kernel(const AttentionArgs a) {
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
+  const int per_head = a.before[a.tiles], share = share_of(a, per_head * a.b.kv_heads);
+  const int rest = blockIdx.x / (BM / 4), head = rest % a.b.kv_heads, tile = rest / a.b.kv_heads, x = (int)(blockIdx.x % (BM / 4)) * 4 + wave;
+  const int n = a.before[tile + 1] - a.before[tile];
+  if (n == 0) return;
+  const int at = head * per_head + a.before[tile], g0 = at / share, g1 = (at + n - 1) / share;
+  if (g0 == g1) return;
+  const Rows r = rows_of<BM>(a, tile, lane);
+  // the first workgroup began the tile, whether or not its share begins with it
+  const auto part = [&](int g, int x) { return ((int64_t)2 * g + (g == g0)) * BM + x; };
+  if (x >= r.count - r.first) return;
+  float top = -__builtin_inff();
+  for (int g = g0 + lane; g <= g1; g += 64) top = fmaxf(top, a.stats[2 * part(g, x)]);
+  top = wave_reduce<MaxF>(top);
+  float sum = 0.0f;
+  f32x4 o{0, 0, 0, 0};
+  for (int base = g0; base <= g1; base += 4) {
+    f32x4 v[4];
+    float f[4];
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+      const int64_t p = part(min(base + i, g1), x);
+      const float cm = base + i <= g1 ? a.stats[2 * p] : -__builtin_inff(), l = a.stats[2 * p + 1];
+      f[i] = cm == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(cm - top);
+      if (f[i] != 0.0f) sum = fmaf(f[i], l, sum);
+      v[i] = f32x4{0, 0, 0, 0};
+      if (4 * lane < a.b.dim) v[i] = *reinterpret_cast<const f32x4 *>(a.part + p * a.b.dim + 4 * lane);
+    }
+#pragma unroll
+    for (int i = 0; i < 4; ++i)
+      if (f[i] != 0.0f) o += v[i] * f[i];
+  }
+  const Place place = place_of(a, r, head, r.first + x, -1, top, sum, lane == 0);
+  if (4 * lane < a.b.dim) place.put<E>(4 * lane, o);
 }
 
 // Up to 32 rows: the waves share them and split the keys, each with a place of its
@@ -550,6 +724,7 @@ __global__ __launch_bounds__(64 * Few<D>::W) void attention_few_kernel(const Att
 
   const int begin = r.lo / KT, all = max(0, (r.hi + KT - 1) / KT - begin), per = (all + a.splits - 1) / a.splits;
   const int t0 = begin + min(split * per, all), t1 = begin + min((split + 1) * per, all);
+  const Parts parts{a.splits > 1 ? (((int64_t)tile * b.kv_heads + head) * a.splits + split) * 32 : -1, 1};
   Tile w;
   w.start(a, r, head, 0, lane);
 
@@ -612,7 +787,7 @@ __global__ __launch_bounds__(64 * Few<D>::W) void attention_few_kernel(const Att
 #pragma unroll
   for (int v = 0; v < W; ++v) bad = bad || any_bad[v];
   if (bad) {
-    rows_one_by_one<E>(a, r, head, split, r.first + wave, r.first + rows, W, t0 * KT, t1 * KT, lane);
+    rows_one_by_one<E>(a, r, head, parts, r.first + wave, r.first + rows, W, t0 * KT, t1 * KT, lane);
     return;
   }
   const int mine_row = lane % 32;
@@ -645,46 +820,44 @@ __global__ __launch_bounds__(64 * Few<D>::W) void attention_few_kernel(const Att
       sum = fmaf(stats[1][v][row], __builtin_amdgcn_exp2f((m - big) * a.c), sum);
       o += *reinterpret_cast<const f32x4 *>(sums + (v * 32 + row) * D + sum_at(row, d / 4));
     }
-    place_of(a, r, head, r.first + row, split, big * a.c, sum, d == 0).put<E>(d, o);
+    place_of(a, r, head, r.first + row, parts.of(row), big * a.c, sum, d == 0).put<E>(d, o);
   }
 }
 
-// The parts of a row's splits joined, a wave to a row.
+// The splits' parts of a tile's 32 rows joined, eight rows to a wave.
 template <typename E>
 __global__ __launch_bounds__(256) void attention_join_kernel(const AttentionArgs a) {
-  const Paged &b = a.b;
-  const int lane = threadIdx.x % 64;
-  const int64_t row = (int64_t)blockIdx.x * 4 + threadIdx.x / 64;
-  if (row >= (int64_t)b.tokens * b.heads) return;
-  const int token = (int)(row / b.heads);
-  if (b.seq_starts && (token < b.seq_starts[0] || token >= b.seq_starts[b.seqs])) return;  // behind the last sequence
-  float cm = -__builtin_inff(), l = 0.0f;
-  if (lane < a.splits) {
-    cm = a.part[a.parts * b.dim + 2 * (row * a.splits + lane)];
-    l = a.part[a.parts * b.dim + 2 * (row * a.splits + lane) + 1];
-  }
-  const float top = wave_reduce<MaxF>(cm);
-  const float f = cm == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(cm - top);
-  const float sum = wave_reduce<SumF>(f == 0.0f ? 0.0f : f * l);
-  // eight splits' parts are in flight; parts of splits without keys may hold anything
-  f32x4 o{0, 0, 0, 0};
-  const float *part = a.part + row * a.splits * b.dim + 4 * lane;
-  for (int base = 0; base < a.splits; base += 8) {
-    f32x4 v[8];
-#pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      v[i] = f32x4{0, 0, 0, 0};
-      if (base + i < a.splits && 4 * lane < b.dim) v[i] = *reinterpret_cast<const f32x4 *>(part + (base + i) * b.dim);
+  const int lane = threadIdx.x % 64, head = blockIdx.x % a.b.kv_heads, tile = blockIdx.x / a.b.kv_heads;
+  const Rows r = rows_of<32>(a, tile, lane);
+  for (int x = threadIdx.x / 64; x < min(32, r.count - r.first); x += 4) {
+    const int64_t first = (int64_t)blockIdx.x * a.splits * 32 + x;
+    float cm = -__builtin_inff(), l = 0.0f;
+    if (lane < a.splits) {
+      cm = a.stats[2 * (first + lane * 32)];
+      l = a.stats[2 * (first + lane * 32) + 1];
     }
+    // eight splits' parts are in flight; those of splits without keys hold zeros
+    f32x4 o{0, 0, 0, 0};
+    const float top = wave_reduce<MaxF>(cm);
+    const float f = cm == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(cm - top);
+    const float sum = wave_reduce<SumF>(f == 0.0f ? 0.0f : f * l);
+    const float *part = a.part + first * a.b.dim + 4 * lane;
+    for (int base = 0; base < a.splits; base += 8) {
+      f32x4 v[8];
 #pragma unroll
-    for (int i = 0; i < 8; ++i) {
-      const float fs = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), (base + i) % 64));
-      if (base + i < a.splits && fs != 0.0f) o += v[i] * fs;
+      for (int i = 0; i < 8; ++i) {
+        v[i] = f32x4{0, 0, 0, 0};
+        if (base + i < a.splits && 4 * lane < a.b.dim) v[i] = *reinterpret_cast<const f32x4 *>(part + (int64_t)(base + i) * 32 * a.b.dim);
+      }
+#pragma unroll
+      for (int i = 0; i < 8; ++i) {
+        const float fs = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), (base + i) % 64));
+        if (base + i < a.splits && fs != 0.0f) o += v[i] * fs;
+      }
     }
+    const Place place = place_of(a, r, head, r.first + x, -1, top, sum, lane == 0);
+    if (4 * lane < a.b.dim) place.put<E>(4 * lane, o);
   }
-  const Place place{a.out + (int64_t)token * a.ldo + row % b.heads * b.dim, nullptr, sum == 0.0f ? 0.0f : 1.0f / sum};
-  if (4 * lane < b.dim) place.put<E>(4 * lane, o);
-  if (a.lse && lane == 0) a.lse[row] = lse_of(top, sum);
 }
 
 }  // namespace fluxbin

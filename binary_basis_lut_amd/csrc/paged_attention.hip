@@ -8,42 +8,76 @@ using namespace fluxbin;
 
 namespace {
 
-constexpr int64_t kTargetGroups = 256;  // one to a CU
-constexpr int64_t kMinKeys = 512;       // of a split
-constexpr int64_t kMaxSplits = 64;      // the join's lanes
 constexpr int64_t kMaxGrid = ((int64_t)1 << 24) - 1;
 
+// Sequences whose new tokens fill at most 32 rows of a key head on average go to
+// the kernel whose waves share the rows and split the keys.  Where such tiles are
+// fewer than fill the chip, the keys are split over workgroups too.
+constexpr int64_t kFewRows = 32;
+constexpr int64_t kMinKeys = 512;   // of a split
+constexpr int64_t kMaxSplits = 64;  // the join's lanes
+
+constexpr int64_t kChunkRows = 128;
+
+// Whether equal shares of the key tiles are faster than a workgroup to a row tile
+// and head: `units` key tiles that every row tile has, `busy` of these, in the times
+// of a key tile measured with one workgroup to a CU and with all that it holds.
+// Counting the shares and joining their parts takes about kJoin.  With 128
+// dimensions, 8 key heads of 8: 517 new tokens over 31000 (264 row tiles and heads) 615
+// us by shares, 822 without; 100 over 30000 108 and 590; 256 over 2000 58 and 56; 512
+// over 4000 120 and 102; without cached tokens, where the first row tiles are short and
+// a share has many, 2000 new 122 and 58.
+constexpr double kJoin = 35.0;  // us
+bool shares_pay(double units, int64_t busy, int64_t shares, int64_t dim) {
+  const double alone = dim <= 64 ? 0.8 : dim <= 128 ? 1.4 : 2.6, full = dim <= 64 ? 1.4 : dim <= 128 ? 2.5 : 2.6;
+  return units * (busy <= 256 ? alone : 0.8 * full) > units * full * (double)busy / (double)shares + kJoin;
+}
+
 struct Plan {
-  int32_t rows, splits;  // rows of a workgroup
-  int64_t tiles;
+  bool few, balanced;
+  int32_t splits, shares;
+  int64_t tiles, parts;  // parts: rows of the workspace
 };
 
-// Sequences whose new tokens fill at most 32 rows of a key head on average go to
-// the kernel whose waves share the rows and split the keys.  Where the tiles are
-// fewer than kTargetGroups, the keys are split over workgroups too.
 Plan plan_of(const fluxbin_paged_batch &b, int64_t window) {
   const int64_t group = b.heads / b.kv_heads, per_seq = b.seqs ? cdiv(b.tokens * group, b.seqs) : 0;
-  Plan p{};
-  p.rows = per_seq <= 32 ? 32 : 128;
-  p.tiles = b.tokens * group / p.rows + b.seqs;
   const int64_t cap = b.table_pages * b.page_size, most = b.max_kv_len ? std::min(b.max_kv_len, cap) : cap;
   const int64_t keys = window ? std::min(most, window + b.tokens) : most;
-  const int64_t busy = std::max<int64_t>(1, b.seqs * cdiv(per_seq, p.rows) * b.kv_heads);
-  p.splits = (int32_t)std::max<int64_t>(1, std::min({kTargetGroups / busy, cdiv(keys, kMinKeys), kMaxSplits}));
+  Plan p{};
+  p.few = per_seq <= kFewRows;
+  p.splits = 1;
+  const int64_t rows = p.few ? kFewRows : kChunkRows;
+  p.tiles = b.tokens * group / rows + b.seqs;
+  const int64_t busy = std::max<int64_t>(1, b.seqs * cdiv(per_seq, rows) * b.kv_heads);
+  if (p.few) {
+    const int64_t room = b.dim <= 64 ? 512 : 256;  // workgroups that the chip's LDS holds
+    p.splits = (int32_t)std::max<int64_t>(1, std::min({room / busy, cdiv(keys, kMinKeys), kMaxSplits}));
+    p.parts = p.splits > 1 ? p.tiles * b.kv_heads * p.splits * kFewRows : 0;
+  } else {
+    p.shares = b.dim <= 128 ? 256 * kChunksPerCu<128> : 256 * kChunksPerCu<256>;
+    p.balanced = busy < p.shares && p.tiles <= kTilesMost && p.tiles * b.kv_heads * cdiv(cap, 32) < (int64_t)1 << 30 &&
+                 shares_pay((double)(keys - cdiv(b.tokens, b.seqs)) / kChunkKeys, busy, p.shares, b.dim);
+    p.parts = p.balanced ? 2 * p.shares * kChunkRows : 0;
+  }
   return p;
 }
 
-size_t ws_bytes(const fluxbin_paged_batch &b, const Plan &p) {
-  return p.splits > 1 ? (size_t)(b.tokens * b.heads * p.splits * (b.dim + 2)) * 4 : 0;
-}
+size_t before_bytes(const Plan &p) { return p.balanced ? (size_t)cdiv((p.tiles + 1) * 4, 256) * 256 : 0; }
+size_t ws_bytes(const fluxbin_paged_batch &b, const Plan &p) { return before_bytes(p) + (size_t)(p.parts * (b.dim + 2)) * 4; }
 
 template <typename E, int D>
 void launch(const AttentionArgs &a, const Plan &p, hipStream_t st) {
   const dim3 grid((unsigned)(p.tiles * p.splits * a.b.kv_heads));
-  if (p.rows == 32) hipLaunchKernelGGL((attention_few_kernel<E, D>), grid, dim3(64 * Few<D>::W), 0, st, a);
-  else hipLaunchKernelGGL((attention_chunk_kernel<E, D, 1>), grid, dim3(256), 0, st, a);
-  if (p.splits > 1)
-    hipLaunchKernelGGL(attention_join_kernel<E>, dim3((unsigned)cdiv((int64_t)a.b.tokens * a.b.heads, 4)), dim3(256), 0, st, a);
+  if (p.few) {
+    hipLaunchKernelGGL((attention_few_kernel<E, D>), grid, dim3(64 * Few<D>::W), 0, st, a);
+    if (p.splits > 1) hipLaunchKernelGGL(attention_join_kernel<E>, dim3((unsigned)(p.tiles * a.b.kv_heads)), dim3(256), 0, st, a);
+  } else if (p.balanced) {
+    hipLaunchKernelGGL((attention_count_kernel<kChunkRows>), dim3(1), dim3(1024), 0, st, a);
+    hipLaunchKernelGGL((attention_balanced_kernel<E, D, 1>), dim3(p.shares), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((attention_gather_kernel<E, kChunkRows>), dim3((unsigned)(p.tiles * a.b.kv_heads * (kChunkRows / 4))), dim3(256), 0, st, a);
+  } else {
+    hipLaunchKernelGGL((attention_chunk_kernel<E, D, 1>), grid, dim3(256), 0, st, a);
+  }
 }
 
 template <typename E>
@@ -61,7 +95,7 @@ fluxbin_status fluxbin_paged_attention_workspace_size(const fluxbin_paged_batch 
   const fluxbin_status st = check_paged(batch);
   if (st) return st;
   if (!bytes) return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "bytes is NULL");
-  *bytes = ws_bytes(*batch, plan_of(*batch, 0));
+  *bytes = ws_bytes(*batch, plan_of(*batch, 0));  // a window never takes more
   return ok();
 }
 
@@ -78,7 +112,7 @@ fluxbin_status fluxbin_paged_attention(const fluxbin_paged_batch *batch, const v
   if ((st = check_rows("out", out, ldo, (int64_t)b.heads * b.dim))) return st;
   if (!aligned(lse, 4)) return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "lse is not aligned to its elements");
   const Plan p = plan_of(b, window);
-  const int64_t grid = p.tiles * p.splits * b.kv_heads;
+  const int64_t grid = p.tiles * b.kv_heads * std::max<int64_t>(p.splits, p.balanced ? kChunkRows / 4 : 1);
   if (grid > kMaxGrid) return fail(FLUXBIN_ERR_UNSUPPORTED, "%lld workgroups are beyond one launch", (long long)grid);
   const size_t need = ws_bytes(b, p);
   if (need && (!workspace || workspace_bytes < need))
@@ -89,14 +123,16 @@ fluxbin_status fluxbin_paged_attention(const fluxbin_paged_batch *batch, const v
   a.q = (const uint16_t *)q;
   a.out = (uint16_t *)out;
   a.lse = lse;
-  a.part = (float *)workspace;
+  a.before = (int32_t *)workspace;
+  a.part = (float *)((char *)workspace + before_bytes(p));
+  a.stats = a.part + p.parts * b.dim;
   a.ldq = ldq;
   a.ldo = ldo;
-  a.parts = b.tokens * b.heads * p.splits;
   a.group = b.heads / b.kv_heads;
   a.window = window;
   a.splits = p.splits;
   a.tiles = (int32_t)p.tiles;
+  a.workgroups = p.shares;
   a.c = scale * 1.44269504088896340736f;
   hipStream_t s = (hipStream_t)stream;
   if (b.dtype == FLUXBIN_DT_F16) run<F16>(a, p, s);

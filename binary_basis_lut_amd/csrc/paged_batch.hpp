@@ -19,24 +19,40 @@ struct Paged {
   int32_t heads, kv_heads, dim, page_shift;
 };
 
-// How many j in [1, n] have start(j) <= at, for a start() that does not decrease;
-// the lanes of a wave each look at one place, so that 4096 sequences take two
-// rounds of loads.
+// A sequence: its number (seqs: none), its first row and the next sequence's, as
+// they are given, and the length of its cache.
+struct Found {
+  int seq, start, next, len;
+};
+
+// The number of j in [1, seqs] for which within(seq_starts[j], j) holds, which is
+// true up to some j, as a sequence.  Up to 63 sequences are looked at in one round
+// of loads, a lane to each; of more, 64 places at a time (4096 take two rounds).
 template <typename F>
-__device__ __forceinline__ int count_starts(int n, int lane, F within) {
-  int lo = 0;
+__device__ __forceinline__ Found find_sequence(const Paged &b, int lane, F within) {
+  Found f;
+  if (b.seqs < 64) {
+    const int start = b.seq_starts ? b.seq_starts[min(lane, b.seqs)] : lane, len = b.kv_lens[min(lane, b.seqs - 1)];
+    f.seq = __popcll(__ballot(lane >= 1 && lane <= b.seqs && within(start, lane)));
+    const int at = min(f.seq, b.seqs - 1);
+    f.start = __builtin_amdgcn_readlane(start, at);
+    f.next = __builtin_amdgcn_readlane(start, at + 1);
+    f.len = __builtin_amdgcn_readlane(len, at);
+    return f;
+  }
+  int lo = 0, n = b.seqs;
   while (n > 0) {
     const int step = (n + 63) / 64, j = (lane + 1) * step;
-    const int c = __popcll(__ballot(j <= n && within(lo + j)));
+    const int c = __popcll(__ballot(j <= n && within(b.seq_starts ? b.seq_starts[lo + j] : lo + j, lo + j)));
     lo += c * step;
     n = min(step - 1, n - c * step);
   }
-  return lo;
-}
-
-// Rows of sequence s, cut to those that exist.
-__device__ __forceinline__ int row_start(const Paged &b, int s) {
-  return b.seq_starts ? max(0, min(b.seq_starts[s], b.tokens)) : s;
+  f.seq = lo;
+  const int at = min(lo, b.seqs - 1);
+  f.start = b.seq_starts ? b.seq_starts[at] : at;
+  f.next = b.seq_starts ? b.seq_starts[at + 1] : at + 1;
+  f.len = b.kv_lens[at];
+  return f;
 }
 
 // The page that holds `index` (>= 0) of sequence s, or -1 where there is none.

@@ -8,33 +8,27 @@ using namespace fluxbin;
 
 namespace {
 
-constexpr int64_t kFewWaves = 2048;  // two to a SIMD
-
-template <typename E, int LPR, int U, bool NORM>
+template <typename E, int C, int LPR>
 void launch(const RopeArgs &a, int rows, bool near, hipStream_t st) {
-  const int step = 64 / LPR * U;
   RopeArgs b = a;
-  // few tokens: a step of rows to a wave, so that all rows of a token are in
-  // flight; else all rows of a token to a wave, which computes its angles once
-  b.rows_per_wave = U == 1 ? step : (int)cdiv(rows, step) * step;
-  const int64_t runs = cdiv(rows, b.rows_per_wave), waves = runs * a.b.tokens;
-  hipLaunchKernelGGL((rope_append_kernel<E, LPR, U, NORM>), dim3((unsigned)cdiv(waves, 4)), dim3(256), 0, st, b, (int)runs, near);
+  b.runs = (int32_t)cdiv(rows, 64 / LPR);
+  const dim3 grid((unsigned)cdiv(b.runs * (int64_t)a.b.tokens, 4)), block(256);
+  if (a.q_norm || a.k_norm) hipLaunchKernelGGL((rope_append_kernel<E, C, LPR, true>), grid, block, 0, st, b, near);
+  else hipLaunchKernelGGL((rope_append_kernel<E, C, LPR, false>), grid, block, 0, st, b, near);
 }
 
-template <typename E, int LPR>
-void choose(const RopeArgs &a, int rows, bool near, hipStream_t st) {
-  const bool norm = a.q_norm || a.k_norm, few = a.b.tokens * cdiv(rows, 64 / LPR) <= kFewWaves;
-  if (norm && few) launch<E, LPR, 1, true>(a, rows, near, st);
-  else if (norm) launch<E, LPR, 4, true>(a, rows, near, st);
-  else if (few) launch<E, LPR, 1, false>(a, rows, near, st);
-  else launch<E, LPR, 4, false>(a, rows, near, st);
+template <typename E, int C>
+void with_lanes(const RopeArgs &a, int rows, bool near, hipStream_t st) {
+  if (a.b.dim <= 8 * C) launch<E, C, 4>(a, rows, near, st);
+  else if (a.b.dim <= 16 * C) launch<E, C, 8>(a, rows, near, st);
+  else if (C == 8 || a.b.dim <= 32 * C) launch<E, C, 16>(a, rows, near, st);
+  else launch<E, C, C == 8 ? 16 : 32>(a, rows, near, st);
 }
 
 template <typename E>
 void run(const RopeArgs &a, int rows, bool near, hipStream_t st) {
-  if (a.b.dim <= 64) choose<E, 8>(a, rows, near, st);
-  else if (a.b.dim <= 128) choose<E, 16>(a, rows, near, st);
-  else choose<E, 32>(a, rows, near, st);
+  if (a.b.dim % 16 == 0 && a.rot % 16 == 0) with_lanes<E, 8>(a, rows, near, st);
+  else with_lanes<E, 4>(a, rows, near, st);
 }
 
 }  // namespace

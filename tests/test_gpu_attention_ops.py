@@ -79,7 +79,7 @@ def test_chunks(fb, dt, dim, heads, kv):
 
 
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
-@pytest.mark.parametrize("lengths", [[(1, 5000)], [(3, 2000)], [(200, 1500)], [(1, 300), (1, 4000), (1, 2)]])
+@pytest.mark.parametrize("lengths", [[(1, 5000)], [(3, 2000)], [(1, 300), (1, 4000), (1, 2)]])
 def test_keys_split_over_workgroups(fb, dt, lengths):
     note(f"splits {dt} {lengths}")
     c = Paged(dt, 4, 1, 128, 16, lengths, seed=5, max_kv_len=8192)
@@ -93,6 +93,27 @@ def test_windows(fb, window, dim):
     for lengths in ([(1, 0), (1, 99), (1, 100), (1, 777)], [(70, 130), (9, 0)], [(5, 1200)]):
         note(f"window {window} dim {dim} {lengths}")
         check(fb, Paged("f16", 4, 2, dim, 32, lengths, seed=window), window=window)
+
+
+BALANCED = [(128, 4, 1, [(200, 3000)]), (64, 2, 2, [(300, 1700), (40, 5), (0, 0), (150, 900)]), (256, 2, 1, [(130, 1500)]),
+            (72, 6, 2, [(90, 2500), (33, 0)]), (128, 2, 1, [(70, 0), (65, 4100)])]
+
+
+def balanced(dt, dim, heads, kv, lengths, seed, page=16, **kw):
+    """A table so long that the host takes the work for large: shares of key tiles are handed out."""
+    rows = -(-sum(n for n, _ in lengths) * (heads // kv) // len(lengths))
+    busy = len(lengths) * -(-rows // 128) * kv
+    return Paged(dt, heads, kv, dim, page, lengths, seed=seed, decode=False, table_extra=(1 << 21) // busy // page + 1, max_kv_len=0, **kw)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("dim,heads,kv,lengths", BALANCED)
+def test_shares_of_key_tiles(fb, dt, dim, heads, kv, lengths):
+    note(f"shares {dt} dim {dim} heads {heads}/{kv} {lengths}")
+    for window, order in ((0, "heads"), (1000, "tokens")):
+        c = balanced(dt, dim, heads, kv, lengths, 7, order=order, behind=3)
+        assert fb.fluxbin_paged_attention_workspace_size(c.upload(fb)) > 0  # without shares a chunk needs none
+        check(fb, c, window=window)
 
 
 def counting(c, seed):
@@ -124,6 +145,39 @@ def test_every_key_counts_once(fb, dt, dim, heads, kv, lengths, window, max_kv):
         # sums of equal weights are exact; the quotient has two roundings, the output one
         assert (np.abs(got - out) <= (UNIT[dt] + 3 * U) * out).all()
         assert (np.abs(ls - lse) <= 4 * U * np.abs(lse) + 4 * U * np.log2(seen + 1.0)[:, None] + 8 * U).all()
+
+
+@pytest.mark.parametrize("dim,heads,kv,lengths", BALANCED)
+def test_every_key_counts_once_in_shares(fb, dim, heads, kv, lengths):
+    note(f"counting in shares, dim {dim} {lengths}")
+    for window in (0, 700):
+        c = balanced("f16", dim, heads, kv, lengths, 2)
+        counting(c, 5)
+        got, ls = attend(fb, c, 0.3, window)
+        out, lse, _, _, seen = attention_oracle(c, 0.3, window)
+        assert (np.abs(got - out) <= (UNIT["f16"] + 3 * U) * out).all()
+        live = seen > 0
+        assert (np.abs(ls - lse) <= 4 * U * np.abs(lse) + 4 * U * np.log2(seen + 1.0)[:, None] + 8 * U)[live].all()
+
+
+def test_shares_with_pages_that_are_not_there_and_values_that_are_not_numbers(fb):
+    note("shares, missing pages and NaN")
+    c = balanced("f16", 128, 4, 1, [(200, 3000), (50, 0)], 3)
+    c.table_host[0, 3:70:2] = -1
+    c.table_host[0, 190:] = c.pages
+    check(fb, c)
+    c = balanced("f16", 128, 4, 1, [(200, 3000)], 4)
+    clean, _ = attend(fb, c, 0.1)
+    out, _, mag, work, seen = attention_oracle(c, 0.1)
+    tol, _ = attention_bounds(c, out, mag, work, seen)
+    last = c.lens_host[0] - 1
+    c.v[c.table_host[0, last // 16], :, last % 16] = math.nan
+    got, _ = attend(fb, c, 0.1)
+    assert np.isnan(got[-1]).all() and (np.abs(got - clean) <= 2 * tol)[:-1].all()
+    c.table_host[:] = -1
+    check(fb, c)
+    c.lens_host = [7]  # shorter than the new tokens
+    check(fb, c)
 
 
 @pytest.mark.parametrize("dim,heads,kv,lengths", [(128, 4, 2, [(1, 200), (1, 90)]), (64, 2, 2, [(100, 60), (40, 0)]),
@@ -204,10 +258,11 @@ def test_large_scores(fb, lengths):
         check(fb, c)
 
 
-@pytest.mark.parametrize("lengths,max_kv", [([(1, 1000)], None), ([(1, 50), (1, 2000)], 4096), ([(300, 100)], None)])
+@pytest.mark.parametrize("lengths,max_kv", [([(1, 1000)], None), ([(1, 50), (1, 2000)], 4096), ([(300, 100)], None),
+                                            ([(300, 2000), (20, 0)], 0)])
 def test_repeats_streams_and_graphs(fb, lengths, max_kv):
     note(f"repeats and graphs {lengths}")
-    c = Paged("bf16", 8, 2, 128, 16, lengths, seed=9, max_kv_len=max_kv)
+    c = balanced("bf16", 128, 8, 2, lengths, 9) if max_kv == 0 else Paged("bf16", 8, 2, 128, 16, lengths, seed=9, max_kv_len=max_kv)
     b = c.upload(fb)
     out = torch.empty_like(c.dev["q"])
     need = fb.fluxbin_paged_attention_workspace_size(b)
