@@ -514,8 +514,10 @@ __device__ __forceinline__ void attend_rows(const AttentionArgs &a, const Rows &
     typename Tile::Weights p;
     w.scores(lds.tile[buf][0], lane, s);
     w.mask(s, border || now != (1u << GROUPS) - 1 || key0 + KT > r.hi, key0, now, lane);
+    __builtin_amdgcn_s_setprio(0);  // the other workgroup's products before this one's weights
     w.weights(a.c, s, p);
     w.add_values(lds.tile[buf][1], lane, p);
+    __builtin_amdgcn_s_setprio(1);
   }
   if (bad) {
     rows_one_by_one<E>(a, r, head, parts, first_row, end_row, 1, t0 * KT, t1 * KT, lane);

@@ -39,8 +39,9 @@ struct Plan {
   int64_t tiles, parts;  // parts: rows of the workspace
 };
 
+// Of a batch with tokens and sequences.
 Plan plan_of(const fluxbin_paged_batch &b, int64_t window) {
-  const int64_t group = b.heads / b.kv_heads, per_seq = b.seqs ? cdiv(b.tokens * group, b.seqs) : 0;
+  const int64_t group = b.heads / b.kv_heads, per_seq = cdiv(b.tokens * group, b.seqs);
   const int64_t cap = b.table_pages * b.page_size, most = b.max_kv_len ? std::min(b.max_kv_len, cap) : cap;
   const int64_t keys = window ? std::min(most, window + b.tokens) : most;
   Plan p{};
@@ -95,7 +96,8 @@ fluxbin_status fluxbin_paged_attention_workspace_size(const fluxbin_paged_batch 
   const fluxbin_status st = check_paged(batch);
   if (st) return st;
   if (!bytes) return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "bytes is NULL");
-  *bytes = ws_bytes(*batch, plan_of(*batch, 0));  // a window never takes more
+  // a window never takes more than none
+  *bytes = batch->tokens && batch->seqs ? ws_bytes(*batch, plan_of(*batch, 0)) : 0;
   return ok();
 }
 

@@ -8,27 +8,32 @@ using namespace fluxbin;
 
 namespace {
 
-template <typename E, int C, int LPR>
-void launch(const RopeArgs &a, int rows, bool near, hipStream_t st) {
-  RopeArgs b = a;
-  b.runs = (int32_t)cdiv(rows, 64 / LPR);
-  const dim3 grid((unsigned)cdiv(b.runs * (int64_t)a.b.tokens, 4)), block(256);
-  if (a.q_norm || a.k_norm) hipLaunchKernelGGL((rope_append_kernel<E, C, LPR, true>), grid, block, 0, st, b, near);
-  else hipLaunchKernelGGL((rope_append_kernel<E, C, LPR, false>), grid, block, 0, st, b, near);
+// Runs of 16 bytes where dim and rotary_dim are made of pairs of them.
+int run_elems(int64_t dim, int64_t rot) { return dim % 16 == 0 && rot % 16 == 0 ? 8 : 4; }
+
+// Lanes to a row, two runs each.
+int row_lanes(int64_t dim, int run) {
+  int lanes = 4;
+  while (2 * run * lanes < dim) lanes *= 2;
+  return lanes;
 }
 
-template <typename E, int C>
-void with_lanes(const RopeArgs &a, int rows, bool near, hipStream_t st) {
-  if (a.b.dim <= 8 * C) launch<E, C, 4>(a, rows, near, st);
-  else if (a.b.dim <= 16 * C) launch<E, C, 8>(a, rows, near, st);
-  else if (C == 8 || a.b.dim <= 32 * C) launch<E, C, 16>(a, rows, near, st);
-  else launch<E, C, C == 8 ? 16 : 32>(a, rows, near, st);
+template <typename E, int C, int LPR>
+void launch(const RopeArgs &a, unsigned grid, bool near, hipStream_t st) {
+  const dim3 block(256);
+  if (a.q_norm || a.k_norm) hipLaunchKernelGGL((rope_append_kernel<E, C, LPR, true>), dim3(grid), block, 0, st, a, near);
+  else hipLaunchKernelGGL((rope_append_kernel<E, C, LPR, false>), dim3(grid), block, 0, st, a, near);
 }
 
 template <typename E>
-void run(const RopeArgs &a, int rows, bool near, hipStream_t st) {
-  if (a.b.dim % 16 == 0 && a.rot % 16 == 0) with_lanes<E, 8>(a, rows, near, st);
-  else with_lanes<E, 4>(a, rows, near, st);
+void run(const RopeArgs &a, unsigned grid, int elems, int lanes, bool near, hipStream_t st) {
+  if (elems == 8 && lanes == 4) launch<E, 8, 4>(a, grid, near, st);
+  else if (elems == 8 && lanes == 8) launch<E, 8, 8>(a, grid, near, st);
+  else if (elems == 8) launch<E, 8, 16>(a, grid, near, st);
+  else if (lanes == 4) launch<E, 4, 4>(a, grid, near, st);
+  else if (lanes == 8) launch<E, 4, 8>(a, grid, near, st);
+  else if (lanes == 16) launch<E, 4, 16>(a, grid, near, st);
+  else launch<E, 4, 32>(a, grid, near, st);
 }
 
 }  // namespace
@@ -56,6 +61,11 @@ extern "C" fluxbin_status fluxbin_rope_append(const fluxbin_paged_batch *batch, 
   if (!aligned(q_norm, 2) || !aligned(k_norm, 2) || !aligned(positions, 4) || !aligned(freq, 8))
     return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "q_norm, k_norm, positions or freq is not aligned to its elements");
   if (rotary_dim && !freq) return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "rotary_dim without freq");
+  const int64_t rows = (q ? b.heads : 0) + 2 * (int64_t)b.kv_heads;
+  const int elems = run_elems(b.dim, rotary_dim), lanes = row_lanes(b.dim, elems);
+  const int64_t runs = cdiv(rows, 64 / lanes), grid = cdiv(runs * b.tokens, 4);
+  if (grid >= (int64_t)1 << 24)
+    return fail(FLUXBIN_ERR_UNSUPPORTED, "%lld tokens of %lld rows are beyond one launch", (long long)b.tokens, (long long)rows);
   RopeArgs a{};
   a.b = paged_of(b);
   a.q = (const uint16_t *)q;
@@ -74,10 +84,10 @@ extern "C" fluxbin_status fluxbin_rope_append(const fluxbin_paged_batch *batch, 
   a.eps = eps;
   a.inv_dim = 1.0f / (float)b.dim;
   a.scale = rope_scale;
-  const int rows = (q ? b.heads : 0) + 2 * b.kv_heads;
+  a.runs = (int32_t)runs;
   hipStream_t s = (hipStream_t)stream;
-  if (b.dtype == FLUXBIN_DT_F16) run<F16>(a, rows, pairs == FLUXBIN_ROPE_NEAR, s);
-  else run<BF16>(a, rows, pairs == FLUXBIN_ROPE_NEAR, s);
+  if (b.dtype == FLUXBIN_DT_F16) run<F16>(a, (unsigned)grid, elems, lanes, pairs == FLUXBIN_ROPE_NEAR, s);
+  else run<BF16>(a, (unsigned)grid, elems, lanes, pairs == FLUXBIN_ROPE_NEAR, s);
   const hipError_t e = hipGetLastError();
   return e != hipSuccess ? hip_fail(e, "rope append launch") : ok();
 }

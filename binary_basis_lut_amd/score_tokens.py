@@ -40,6 +40,59 @@ def _row_stride(t) -> int:
     return t.stride(0) if t.shape[0] > 1 else t.shape[1]  # a single row's stride can be any number
 
 
+class LogitRules:
+    """What stands between a head's logits and a choice among them, for up to max_rows rows (fluxbin_adjust_logits).
+
+    A history of up to max_history tokens to a row, kept here: `history` int32 [max_rows][max_history] and
+    `total_len` int32 [max_rows], of which the first prompt_len (int32 [max_rows], None: 0) were given.
+    repetition, frequency, presence: fp32 [max_rows] or None; bias_index int32 and bias_value fp32
+    [max_rows][n] or None; mask: int32 [max_rows][ceil(vocab / 32)] or None, a bit to a token, 0: forbidden.
+    All of it lies on `device` and is read when the work runs, so the caller may change the values between two
+    replays of a graph.
+    """
+
+    def __init__(self, max_rows: int, vocab: int, max_history: int, prompt_len=None, repetition=None, frequency=None, presence=None,
+                 bias_index=None, bias_value=None, mask=None, device="cuda"):
+        import torch
+
+        dev = torch.device(device)
+        self.device = dev = torch.device(dev.type, torch.cuda.current_device()) if dev.index is None else dev
+        self.max_rows, self.vocab, self.max_history = max_rows, vocab, max_history
+        if (bias_index is None) != (bias_value is None):
+            raise ValueError("bias_index and bias_value go together")
+        biases = self.biases = 0 if bias_index is None else bias_index.shape[1]
+        for name, t, dtype, shape in (("prompt_len", prompt_len, torch.int32, (max_rows,)), ("repetition", repetition, torch.float32, (max_rows,)),
+                                      ("frequency", frequency, torch.float32, (max_rows,)), ("presence", presence, torch.float32, (max_rows,)),
+                                      ("bias_index", bias_index, torch.int32, (max_rows, biases)),
+                                      ("bias_value", bias_value, torch.float32, (max_rows, biases)),
+                                      ("mask", mask, torch.int32, (max_rows, (vocab + 31) // 32))):
+            if t is not None:
+                _check(name, t, dtype, dev, shape)
+                if not t.is_contiguous():
+                    raise ValueError(f"{name}: not contiguous")
+        self.prompt_len, self.repetition, self.frequency, self.presence = prompt_len, repetition, frequency, presence
+        self.bias_index, self.bias_value, self.mask = bias_index, bias_value, mask
+        self.history = torch.full((max_rows, max_history), -1, dtype=torch.int32, device=dev)
+        self.total_len = torch.zeros(max_rows, dtype=torch.int32, device=dev)
+
+    def clear(self) -> None:
+        self.total_len.zero_()
+
+    def append(self, tokens) -> None:
+        """tokens: int64 [max_rows][n] behind each row's history (its last place is written again once it is full)."""
+        import torch
+
+        n = tokens.shape[1]
+        at = self.total_len[:, None] + torch.arange(n, device=self.device)
+        self.history.scatter_(1, at.clamp(max=self.max_history - 1), tokens.to(torch.int32))
+        self.total_len.add_(n).clamp_(max=self.max_history)
+
+    def apply(self, logits, ld: int, dtype: int, rows: int, F) -> None:
+        F.fluxbin_adjust_logits(logits, ld, dtype, rows, self.vocab, self.history, self.max_history, self.max_history, self.prompt_len,
+                                self.total_len, self.repetition, self.frequency, self.presence, self.bias_index, self.bias_value,
+                                self.biases, self.biases, self.mask, (self.vocab + 31) // 32, logits, ld)
+
+
 class ScoringHead:
     """Final norm, int8 output head and scoring for up to `max_rows` rows at a time.
 
@@ -80,8 +133,11 @@ class ScoringHead:
         self.workspace = empty(max(need, 16), dtype=torch.uint8)
         torch.cuda.current_stream().synchronize()  # the quantised head is there for a score() on any stream
 
-    def score(self, y, residual, targets, logit_scale: float = 1.0) -> dict:
-        """y, residual: fp16 [rows][hidden], any row stride; targets: int64 [rows], any stride, negative where there is none."""
+    def score(self, y, residual, targets, logit_scale: float = 1.0, rules: LogitRules | None = None) -> dict:
+        """y, residual: fp16 [rows][hidden], any row stride; targets: int64 [rows], any stride, negative where there is none.
+
+        rules: applied to the logits, in place, before they are scored; rows 0 .. of the rules are those of y.
+        """
         import torch
 
         F, rows = self.F, y.shape[0]
@@ -91,12 +147,16 @@ class ScoringHead:
         _check("residual", residual, torch.float16, self.device, (rows, self.hidden))
         _check("targets", targets, torch.int64, self.device, (rows,))
         _check_current(self.device)
+        if rules is not None and (rules.vocab != self.vocab or rules.max_rows < rows or rules.device != self.device):
+            raise ValueError(f"rules: for {rules.max_rows} rows of {rules.vocab} on {rules.device}, not {rows} of {self.vocab} on {self.device}")
         if not targets.is_contiguous():  # one step's column of a [rows][steps] matrix
             targets = self.targets[:rows].copy_(targets)
         F.fluxbin_add_rmsnorm(y, _row_stride(y), residual, _row_stride(residual), self.norm_weight, F.DT_F16, rows, self.hidden,
                               self.eps, self.residual, self.hidden, None, 0, self.q, self.ld, self.scale)
         F.fluxbin_gemm_w8a8(self.q, self.ld, self.scale, self.head_q, self.ld, self.head_scale, None, rows, self.vocab,
                             self.hidden, self.logits, self.vocab, F.DT_F32)
+        if rules is not None:
+            rules.apply(self.logits, self.vocab, F.DT_F32, rows, F)
         F.fluxbin_token_logprobs(self.logits, self.vocab, F.DT_F32, rows, self.vocab, logit_scale, targets, self.logprob,
                                  self.entropy, self.top_k, self.top_logprob, self.top_index, self.workspace,
                                  self.workspace.numel())

@@ -555,7 +555,8 @@ typedef struct {
   int32_t dtype;                 /* of q, k, v, out and the cache: FLUXBIN_DT_F16 or _BF16 */
   int32_t heads, kv_heads, dim;  /* dim a multiple of 8, at most 256; heads at most 1024 */
   int32_t page_size;             /* a power of two, 16 .. 65536 */
-  int64_t tokens, seqs;          /* rows of q; sequences.  At most 2^24, and tokens * heads at most 2^30 */
+  int64_t tokens, seqs;          /* rows of q; sequences.  At most 2^24, and tokens * heads at most 2^30 (what one
+                                    launch cannot do is refused before that) */
   int64_t max_kv_len;            /* what no kv_lens[s] passes (0: table_pages * page_size).  It decides how the
                                     work is divided, not what is computed */
   const int32_t *seq_starts, *kv_lens, *page_table;
@@ -600,8 +601,10 @@ fluxbin_status fluxbin_rope_append(const fluxbin_paged_batch *batch, const void 
  * Products are taken in dtype's matrix instructions with fp32 sums; the
  * weights exp(z - max), at most 2^15, are rounded to dtype for the second.
  * out may not overlap q.  workspace: at least
- * fluxbin_paged_attention_workspace_size() bytes, 16-byte aligned, free for
- * other use once the call's work has finished; NULL where that size is 0. */
+ * fluxbin_paged_attention_workspace_size() bytes (never above 72 MiB), 16-byte
+ * aligned, free for other use once the call's work has finished; NULL where
+ * that size is 0.  One call at a time per workspace: graphs that share one are
+ * replayed one after the other. */
 fluxbin_status fluxbin_paged_attention_workspace_size(const fluxbin_paged_batch *batch, size_t *bytes);
 fluxbin_status fluxbin_paged_attention(const fluxbin_paged_batch *batch, const void *q, int64_t ldq, float scale, int32_t window,
                                        void *out, int64_t ldo, float *lse, void *workspace, size_t workspace_bytes,
