@@ -237,17 +237,18 @@ struct WaveTile {
 
   __device__ __forceinline__ void scores(const int8_t *kt, int lane, Scores &s) const {
 #pragma unroll
-    for (int k = 0; k < KB; ++k) {
+    for (int k = 0; k < KB; ++k)
 #pragma unroll
       for (int x = 0; x < QB; ++x) s[k][x] = f32x16{};
 #pragma unroll
-      for (int i = 0; i < STEPS; ++i) {
+    for (int i = 0; i < STEPS; ++i)
+#pragma unroll
+      for (int k = 0; k < KB; ++k) {
         const int row = 32 * k + lane % 32;
         const u32x4 f = *reinterpret_cast<const u32x4 *>(kt + row * D * 2 + k_place<D>(row, 2 * i + lane / 32) * 16);
 #pragma unroll
         for (int x = 0; x < QB; ++x) s[k][x] = multiply<E>(f, q[x][i], s[k][x]);
       }
-    }
   }
 
   // Scores to weights, with what that does to m, l and o.
@@ -314,18 +315,27 @@ struct WaveTile {
   // known there only, which keeps the compiler from doing that work always.)
   __device__ __forceinline__ void mask(Scores &s, bool part, int key0, uint32_t there, int lane) const {
     if (part) {
-      int mine = key0 + 4 * (lane / 32);
-      asm volatile("" : "+v"(mine));
 #pragma unroll
-      for (int k = 0; k < KB; ++k)
+      for (int x = 0; x < QB; ++x) {
+        // The lane's key 0 is number `mine`; keys lo .. lo + span behind it are seen,
+        // one unsigned comparison each (lo out of reach: none).
+        int mine = key0 + 4 * (lane / 32);
+        asm volatile("" : "+v"(mine));
+        const bool any = p[x] >= mine && from[x] <= p[x];
+        const int lo = any ? max(from[x] - mine, 0) : 1 << 20;
+        const uint32_t span = any ? (uint32_t)(p[x] - mine - lo) : 0;
 #pragma unroll
-        for (int x = 0; x < QB; ++x)
+        for (int k = 0; k < KB; ++k)
 #pragma unroll
-          for (int i = 0; i < 16; ++i) {
-            const int key = mine + 32 * k + 8 * (i / 4) + i % 4;
-            const bool seen = key >= from[x] && key <= p[x] && (there >> (2 * k + i / 8) & 1);
-            s[k][x][i] = seen ? s[k][x][i] : -__builtin_inff();
-          }
+          for (int i = 0; i < 16; ++i)
+            s[k][x][i] = (uint32_t)(32 * k + 8 * (i / 4) + i % 4 - lo) <= span ? s[k][x][i] : -__builtin_inff();
+        if (there != (1u << (2 * KB)) - 1) {
+#pragma unroll
+          for (int k = 0; k < KB; ++k)
+#pragma unroll
+            for (int i = 0; i < 16; ++i) s[k][x][i] = there >> (2 * k + i / 8) & 1 ? s[k][x][i] : -__builtin_inff();
+        }
+      }
     }
   }
 
@@ -346,16 +356,19 @@ struct WaveTile {
     return v;
   }
 
-  // Whether the tile holds a value that times 0 is not 0.
+  // Whether the tile holds a value that times 0 is not 0: the largest magnitude, two
+  // values of 16 bits at a time as integers, whose order is theirs.
   static __device__ __forceinline__ bool unclean(const int8_t *vt, int lane) {
-    constexpr uint32_t e = __is_same(E, F16) ? 0x7c00u : 0x7f80u;
-    bool bad = false;
-    for (int at = lane * 16; at < KT * D * 2; at += 1024) {
-      const u32x4 v = *reinterpret_cast<const u32x4 *>(vt + at);
+    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
+    constexpr uint16_t none = __is_same(E, F16) ? 0x7c00u : 0x7f80u;
+    u16x2 top{0, 0};
 #pragma unroll
-      for (int i = 0; i < 4; ++i) bad = bad || (v[i] & e) == e || (v[i] >> 16 & e) == e;
+    for (int at = 0; at < KT * D * 2; at += 1024) {
+      const u32x4 v = *reinterpret_cast<const u32x4 *>(vt + at + lane * 16);
+#pragma unroll
+      for (int i = 0; i < 4; ++i) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, v[i] & 0x7fff7fffu));
     }
-    return __any(bad);
+    return __any(top[0] >= none || top[1] >= none);
   }
 };
 
