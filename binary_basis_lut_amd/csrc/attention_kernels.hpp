@@ -8,7 +8,10 @@
 // when a score passes it by more than kSlack (in powers of two), so weights reach
 // 2^15; the factor 2^7 keeps small ones out of fp16's subnormals.  Weights are
 // rounded to the activation type for the second product alone: l, and with it lse,
-// is the fp32 sum of the weights before that.  Two sets of keys are joined by moving both to the larger m, so keys
+// is the fp32 sum of the weights before that.  That rounding of every weight adds
+// about as much to an output's error as the output's own (in quadrature); a chunk's
+// products are what bounds it and bear no more, single tokens wait for memory and
+// take a second product with what the rounding left.  Two sets of keys are joined by moving both to the larger m, so keys
 // may be split over waves and workgroups.
 //
 // All rows that read one key head are rows of one matrix: row r of a sequence is
@@ -251,7 +254,7 @@ struct WaveTile {
       }
   }
 
-  // Scores to weights, with what that does to m, l and o.
+  // Scores to weights, which stay in s unrounded, with what that does to m, l and o.
   __device__ __forceinline__ void weights(float c, Scores &s, Weights &w) {
     float top[QB];
     bool rise = false;
@@ -289,6 +292,8 @@ struct WaveTile {
           for (int i = 0; i < 4; ++i) {
             const float a = __builtin_amdgcn_exp2f(fmaf(s[k][x][8 * j + 2 * i], c, shift));
             const float b = __builtin_amdgcn_exp2f(fmaf(s[k][x][8 * j + 2 * i + 1], c, shift));
+            s[k][x][8 * j + 2 * i] = a;
+            s[k][x][8 * j + 2 * i + 1] = b;
             w[k][j][x][i] = pair_of<E>(a, b);
             sum[i % 2] += a + b;
           }
@@ -296,7 +301,23 @@ struct WaveTile {
     }
   }
 
-  __device__ __forceinline__ void add_values(const int8_t *vt, int lane, const Weights &w) {
+  // weights() with what its roundings leave, rounded in its turn, in `rest`.
+  __device__ __forceinline__ void exact_weights(float c, Scores &s, Weights &w, Weights &rest) {
+    weights(c, s, w);
+#pragma unroll
+    for (int k = 0; k < KB; ++k)
+#pragma unroll
+      for (int j = 0; j < 2; ++j)
+#pragma unroll
+        for (int x = 0; x < QB; ++x)
+#pragma unroll
+          for (int i = 0; i < 4; ++i) {
+            const uint32_t v = w[k][j][x][i];
+            rest[k][j][x][i] = pair_of<E>(s[k][x][8 * j + 2 * i] - E::load((uint16_t)v), s[k][x][8 * j + 2 * i + 1] - E::load((uint16_t)(v >> 16)));
+          }
+  }
+
+  __device__ __forceinline__ void add_values(const int8_t *vt, int lane, const Weights &w, const Weights *rest = nullptr) {
 #pragma unroll
     for (int k = 0; k < KB; ++k)
 #pragma unroll
@@ -305,7 +326,10 @@ struct WaveTile {
         for (int i = 0; i < DB; ++i) {
           const u32x4 v = values(vt, 32 * k + 16 * j, i, lane);
 #pragma unroll
-          for (int x = 0; x < QB; ++x) o[i][x] = multiply<E>(v, w[k][j][x], o[i][x]);
+          for (int x = 0; x < QB; ++x) {
+            o[i][x] = multiply<E>(v, w[k][j][x], o[i][x]);
+            if (rest) o[i][x] = multiply<E>(v, (*rest)[k][j][x], o[i][x]);
+          }
         }
   }
 
@@ -356,19 +380,17 @@ struct WaveTile {
     return v;
   }
 
-  // Whether the tile holds a value that times 0 is not 0: the largest magnitude, two
-  // values of 16 bits at a time as integers, whose order is theirs.
-  static __device__ __forceinline__ bool unclean(const int8_t *vt, int lane) {
-    typedef uint16_t u16x2 __attribute__((ext_vector_type(2)));
-    constexpr uint16_t none = __is_same(E, F16) ? 0x7c00u : 0x7f80u;
-    u16x2 top{0, 0};
+  // Whether an infinity or NaN has come into o: one among the values, which a weight
+  // of 0 turns into NaN for rows that do not see it, or one among the scores.
+  __device__ __forceinline__ bool unclean() const {
+    float z = 0.0f;
 #pragma unroll
-    for (int at = 0; at < KT * D * 2; at += 1024) {
-      const u32x4 v = *reinterpret_cast<const u32x4 *>(vt + at + lane * 16);
+    for (int i = 0; i < DB; ++i)
 #pragma unroll
-      for (int i = 0; i < 4; ++i) top = __builtin_elementwise_max(top, __builtin_bit_cast(u16x2, v[i] & 0x7fff7fffu));
-    }
-    return __any(top[0] >= none || top[1] >= none);
+      for (int x = 0; x < QB; ++x)
+#pragma unroll
+        for (int e = 0; e < 16; ++e) z = fmaf(o[i][x][e], 0.0f, z);
+    return __any(!(z == 0.0f));
   }
 };
 
@@ -414,9 +436,8 @@ struct Parts {
 
 // Rows [from, to) of a workgroup over the keys [k0, k1), one after the other by a
 // wave: 64 keys at a time, a lane to a key, then a lane to four dimensions.  For
-// infinities and NaN among values that some rows see and others do not, which a
-// matrix product would carry to all of them (0 times infinity): here a key whose
-// weight is 0 is left out.
+// rows that an infinity or NaN came into: a matrix product carries one to all its
+// rows (0 times infinity); here a key whose weight is 0 is left out.
 template <typename E>
 __device__ __forceinline__ void rows_one_by_one(const AttentionArgs &a, const Rows &r, int head, const Parts &parts, int from, int to, int step,
                                                 int k0, int k1, int lane) {
@@ -435,7 +456,13 @@ __device__ __forceinline__ void rows_one_by_one(const AttentionArgs &a, const Ro
       float s = -__builtin_inff();
       if (page >= 0) {
         s = 0.0f;
-        for (int d = 0; d < b.dim; ++d) s = fmaf(E::load(b.k[at + d]), E::load(q[d]), s);
+#pragma unroll 4
+        for (int d = 0; d < b.dim; d += 8) {
+          const words4 x = *reinterpret_cast<const words4 *>(b.k + at + d), y = *reinterpret_cast<const words4 *>(q + d);
+#pragma unroll
+          for (int i = 0; i < 8; ++i)
+            s = fmaf(E::load((uint16_t)(x[i / 2] >> (16 * (i % 2)))), E::load((uint16_t)(y[i / 2] >> (16 * (i % 2)))), s);
+        }
       }
       const float top = fmaxf(m, wave_reduce<MaxF>(s));
       if (__any(s != s)) l = __builtin_nanf("");
@@ -445,12 +472,22 @@ __device__ __forceinline__ void rows_one_by_one(const AttentionArgs &a, const Ro
       const float w = __builtin_amdgcn_exp2f(fmaf(s, a.c, kWeightShift - m * a.c));
       l = fmaf(l, factor, wave_reduce<SumF>(w));
       o *= factor;
-      for (int j = 0; j < 64; ++j) {
-        const float wj = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), j));
-        if (wj == 0.0f) continue;
-        const int64_t v = (int64_t)__shfl((int)(at >> 32), j) << 32 | (uint32_t)__shfl((int)at, j);
-        if (4 * lane < b.dim)
-          for (int i = 0; i < 4; ++i) o[i] = fmaf(wj, E::load(b.v[v + 4 * lane + i]), o[i]);
+      for (int j0 = 0; j0 < 64; j0 += 8) {
+        words2 x[8];
+        float wj[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+          wj[j] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), j0 + j));
+          const int64_t v = (int64_t)__builtin_amdgcn_readlane((int)(at >> 32), j0 + j) << 32 | (uint32_t)__builtin_amdgcn_readlane((int)at, j0 + j);
+          x[j] = words2{0, 0};
+          if (wj[j] != 0.0f && 4 * lane < b.dim) x[j] = *reinterpret_cast<const words2 *>(b.v + v + 4 * lane);
+        }
+#pragma unroll
+        for (int j = 0; j < 8; ++j)
+          if (wj[j] != 0.0f) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) o[i] = fmaf(wj[j], E::load((uint16_t)(x[j][i / 2] >> (16 * (i % 2)))), o[i]);
+          }
       }
     }
     const Place place = place_of(a, r, head, row, parts.of(row - r.first), m * a.c, l, lane == 0);
@@ -512,7 +549,6 @@ __device__ __forceinline__ void attend_rows(const AttentionArgs &a, const Rows &
   if (tiles > 0) fetch(0);
   find_pages(1);
   const int first_row = r.first + wave * 32 * QB, end_row = min(first_row + 32 * QB, r.count);
-  bool bad = false;
   for (int n = 0; n < tiles; ++n) {
     const int buf = n % 2, key0 = tile_at(n) * KT;
     wait_and_meet<0>();
@@ -522,7 +558,6 @@ __device__ __forceinline__ void attend_rows(const AttentionArgs &a, const Rows &
     if (n + 1 < tiles) fetch(n + 1);
     find_pages(n + 2);
     const bool border = key0 + KT - 1 > r.p_lo || (a.window && key0 <= r.p_hi - a.window);
-    if (border && r.p_lo != r.p_hi) bad = bad || w.unclean(lds.tile[buf][1], lane);
     typename Tile::Scores s;
     typename Tile::Weights p;
     w.scores(lds.tile[buf][0], lane, s);
@@ -532,7 +567,7 @@ __device__ __forceinline__ void attend_rows(const AttentionArgs &a, const Rows &
     w.add_values(lds.tile[buf][1], lane, p);
     __builtin_amdgcn_s_setprio(1);
   }
-  if (bad) {
+  if (w.unclean()) {
     rows_one_by_one<E>(a, r, head, parts, first_row, end_row, 1, t0 * KT, t1 * KT, lane);
     return;
   }
@@ -764,7 +799,6 @@ __global__ __launch_bounds__(64 * Few<D>::W) void attention_few_kernel(const Att
       pages = t < t1 ? page_of(b, r.seq, t * KT + 16 * (lane % 2)) : -1;
     }
   };
-  bool bad = false;
   find_pages(0);
   fetch(0, b.k, off_k, kt);
   fetch(0, b.v, off_v, vt);
@@ -774,17 +808,16 @@ __global__ __launch_bounds__(64 * Few<D>::W) void attention_few_kernel(const Att
     const bool border = key0 + KT - 1 > r.p_lo || (a.window && key0 <= r.p_hi - a.window);
     const uint32_t there = (page(n, 0) >= 0) | (page(n, 1) >= 0) << 1;
     typename Tile::Scores s;
-    typename Tile::Weights p;
+    typename Tile::Weights p, rest;
     find_pages(n + 1);
     wait_for_loads<2 * Loads::kLoads>();
     w.scores(kt, lane, s);
     wait_for_reads();
     fetch(n + 1, b.k, off_k, kt);
     w.mask(s, border || there != 3 || key0 + KT > r.hi, key0, there, lane);
-    w.weights(a.c, s, p);
+    w.exact_weights(a.c, s, p, rest);
     wait_for_loads<2 * Loads::kLoads>();
-    if (border && r.p_lo != r.p_hi) bad = bad || w.unclean(vt, lane);
-    w.add_values(vt, lane, p);
+    w.add_values(vt, lane, p, &rest);
     wait_for_reads();
     fetch(n + 1, b.v, off_v, vt);
   }
@@ -796,6 +829,7 @@ __global__ __launch_bounds__(64 * Few<D>::W) void attention_few_kernel(const Att
     stats[0][wave][lane] = w.m[0];
     stats[1][wave][lane] = l;
   }
+  bool bad = w.unclean();
   if (lane == 0) any_bad[wave] = bad;
   __syncthreads();
   const int rows = min(32, r.count - r.first);

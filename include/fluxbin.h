@@ -599,7 +599,10 @@ fluxbin_status fluxbin_rope_append(const fluxbin_paged_batch *batch, const void 
  * and NaN too.  lse (fp32 [tokens][heads], natural logarithm) may be NULL; with
  * it, parts computed apart can be joined.  scale is positive and finite.
  * Products are taken in dtype's matrix instructions with fp32 sums; the
- * weights exp(z - max), at most 2^15, are rounded to dtype for the second.
+ * weights exp(z - max), times a power of two and at most 2^15, are rounded to
+ * dtype for the second (where sequences have few rows, in two parts).  Rows that
+ * share a workgroup with an infinite or NaN key or value are computed again one
+ * by one, slowly.  bf16 values beyond 2^100 overflow the sums.
  * out may not overlap q.  workspace: at least
  * fluxbin_paged_attention_workspace_size() bytes (never above 72 MiB), 16-byte
  * aligned, free for other use once the call's work has finished; NULL where

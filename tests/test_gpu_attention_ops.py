@@ -245,6 +245,26 @@ def test_what_a_row_does_not_see_does_not_matter(fb, dt, dim, heads, kv, lengths
     assert np.isnan(got[row]).all() and np.isnan(ls[row]).all() and np.isfinite(got[others]).all()
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("dim,heads,kv,lengths", [(128, 4, 2, [(1, 300), (1, 20)]), (64, 4, 2, [(130, 100)]), (256, 2, 1, [(70, 200)])])
+def test_values_without_bounds_that_rows_do_see(fb, dt, dim, heads, kv, lengths):
+    """An infinity among the values of an old key: its dimension is infinite, the others are as they were."""
+    note(f"infinite values that are seen {dt} dim {dim} {lengths}")
+    c = Paged(dt, heads, kv, dim, 16, lengths, seed=12, decode=False)
+    clean, _ = attend(fb, c, 0.1)
+    out, _, mag, work, seen = attention_oracle(c, 0.1)
+    tol, _ = attention_bounds(c, out, mag, work, seen)
+    p = c.table_host[0, 0]
+    c.v[p, 0, 5, 3], c.v[p, 0, 6, 4], c.v[p, 0, 7, 5], c.v[p, 0, 8, 5] = math.inf, -math.inf, math.inf, -math.inf
+    got, _ = attend(fb, c, 0.1)
+    rows, mine = np.arange(lengths[0][0]), np.arange(heads // kv)
+    want = clean.copy()
+    for d, v in ((3, math.inf), (4, -math.inf), (5, math.nan)):
+        want[np.ix_(rows, mine, [d])] = v
+    same = (np.abs(got - want) <= 2 * tol) | (got == want) | (np.isnan(got) & np.isnan(want))
+    assert same.all(), np.argwhere(~same)[:5]
+
+
 @pytest.mark.parametrize("lengths", [[(1, 300)], [(130, 100)]])
 def test_large_scores(fb, lengths):
     """Scores far apart and large: the weights of all but the largest vanish, and the maximum moves often."""
