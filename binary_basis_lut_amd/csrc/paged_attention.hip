@@ -8,7 +8,7 @@ using namespace fluxbin;
 
 namespace {
 
-constexpr int64_t kMaxGrid = ((int64_t)1 << 24) - 1;
+constexpr int64_t kMaxGrid = ((int64_t)1 << 23) - 1;  // of 512 threads, HIP takes fewer than 2^32
 
 // Sequences whose new tokens fill at most 32 rows of a key head on average go to
 // the kernel whose waves share the rows and split the keys.  Where such tiles are

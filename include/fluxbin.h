@@ -597,7 +597,8 @@ fluxbin_status fluxbin_rope_append(const fluxbin_paged_batch *batch, const void 
  * A row without any key (or with z = -inf for all of them) has out = 0 and
  * lse = -inf.  Keys outside J take no part, whatever they hold, infinities
  * and NaN too.  lse (fp32 [tokens][heads], natural logarithm) may be NULL; with
- * it, parts computed apart can be joined.  scale is positive and finite.
+ * it, parts computed apart can be joined.  scale is positive and at most 1e30;
+ * z is meant to stay in fp32's range.
  * Products are taken in dtype's matrix instructions with fp32 sums; the
  * weights exp(z - max), times a power of two and at most 2^15, are rounded to
  * dtype for the second (where sequences have few rows, in two parts).  Rows that

@@ -130,7 +130,7 @@ def test_nothing_to_do_is_no_error(fb):
 
 def shapes():
     for tokens, seqs in ((1, 1), (2, 1), (7, 7), (64, 64), (300, 300), (4096, 4096), (40, 5), (517, 1), (4096, 1), (9000, 12), (70000, 400),
-                         (3, 900), (1 << 20, 3), (1 << 24, 1 << 24)):
+                         (3, 900), (1 << 20, 3), (5000000, 5000000), (8200000, 8200000), (9000000, 9000000), (1 << 24, 1 << 24)):
         for heads, kv in ((1, 1), (8, 1), (64, 8), (32, 32), (48, 48), (512, 4)):
             if tokens * heads <= 1 << 30:
                 for dim in (8, 64, 128, 136, 256):
@@ -161,7 +161,7 @@ def test_grids_fit_or_are_refused(fb):
         assert r["status"] in (0, 2), (call, r)
         refusals += r["status"] == 2
         assert bool(r["launches"]) == (r["status"] == 0) and all(fits(x) for x in r["launches"]), (call, r)
-    assert 0 < refusals < len(calls) // 4
+    assert 0 < refusals < len(calls) // 2
 
 
 # every kernel of the operators and a call that takes it

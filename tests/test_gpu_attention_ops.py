@@ -87,6 +87,24 @@ def test_keys_split_over_workgroups(fb, dt, lengths):
     check(fb, c)
 
 
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("heads,kv,lengths", [(64, 1, [(1, 300), (1, 7)]), (40, 1, [(1, 130)]), (33, 1, [(2, 90), (1, 0), (4, 9)]),
+                                              (48, 2, [(3, 40)]), (16, 1, [(2, 100), (2, 0)])])
+def test_many_query_heads_to_a_key_head(fb, dt, heads, kv, lengths):
+    """More rows of single tokens than 32, exactly 32, and tiles that begin inside a group."""
+    note(f"{heads} heads to {kv}, {dt} {lengths}")
+    for dim in (64, 128):
+        check(fb, Paged(dt, heads, kv, dim, 32, lengths, seed=heads, order="tokens"))
+
+
+def test_lengths_that_the_host_does_not_know_of(fb):
+    """max_kv_len only divides the work: sequences may be longer or shorter."""
+    note("max_kv_len too small and too large")
+    for max_kv in (1, 100, 1 << 20):
+        for lengths in ([(1, 900), (1, 0)], [(1, 3000)], [(150, 2000)]):
+            check(fb, Paged("f16", 4, 2, 64, 16, lengths, seed=max_kv, max_kv_len=max_kv, table_extra=100))
+
+
 @pytest.mark.parametrize("window", [1, 2, 31, 100, 1000])
 @pytest.mark.parametrize("dim", [64, 128, 256])
 def test_windows(fb, window, dim):
