@@ -706,43 +706,62 @@ __global__ __launch_bounds__(256, kChunksPerCu<D>) void attention_balanced_kerne
   }
 }
 
-// The parts of the row tiles that several workgroups had, joined; a row to a wave.
+// The parts of the row tiles that several workgroups had, joined.  A wave has two
+// rows, or two pairs of them where half its lanes hold a row, and loads four parts of
+// each at once (a row to a wave takes 22 us instead of 12 for 4136 rows of 8 heads:
+// each wave looks its tile up before it loads).
+constexpr int kGatherRows = 2;
 template <typename E, int BM>
 __global__ __launch_bounds__(256) void attention_gather_kernel(const AttentionArgs a) {
-  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64;
-  const int per_head = a.before[a.tiles], share = share_of(a, per_head * a.b.kv_heads);
-  const int rest = blockIdx.x / (BM / 4), head = rest % a.b.kv_heads, tile = rest / a.b.kv_heads, x = (int)(blockIdx.x % (BM / 4)) * 4 + wave;
+  const Paged &b = a.b;
+  const int lane = threadIdx.x % 64, wave = threadIdx.x / 64, pair = b.dim <= 128 ? 2 : 1;
+  const int per_head = a.before[a.tiles], share = share_of(a, per_head * b.kv_heads);
+  const int blocks = BM / (4 * kGatherRows * pair), rest = blockIdx.x / blocks, head = rest % b.kv_heads, tile = rest / b.kv_heads;
   const int n = a.before[tile + 1] - a.before[tile];
   if (n == 0) return;
   const int at = head * per_head + a.before[tile], g0 = at / share, g1 = (at + n - 1) / share;
   if (g0 == g1) return;
   const Rows r = rows_of<BM>(a, tile, lane);
-  // the first workgroup began the tile, whether or not its share begins with it
-  const auto part = [&](int g, int x) { return ((int64_t)2 * g + (g == g0)) * BM + x; };
-  if (x >= r.count - r.first) return;
-  float top = -__builtin_inff();
-  for (int g = g0 + lane; g <= g1; g += 64) top = fmaxf(top, a.stats[2 * part(g, x)]);
-  top = wave_reduce<MaxF>(top);
-  float sum = 0.0f;
-  f32x4 o{0, 0, 0, 0};
-  for (int base = g0; base <= g1; base += 4) {
-    f32x4 v[4];
-    float f[4];
+  const int d = 4 * (lane % (64 / pair)), rows = min(BM, r.count - r.first);
+  const int first = ((int)(blockIdx.x % blocks) * 4 + wave) * kGatherRows * pair + lane / (64 / pair);
+  float m[kGatherRows], sum[kGatherRows];
+  f32x4 o[kGatherRows];
 #pragma unroll
-    for (int i = 0; i < 4; ++i) {
-      const int64_t p = part(min(base + i, g1), x);
-      const float cm = base + i <= g1 ? a.stats[2 * p] : -__builtin_inff(), l = a.stats[2 * p + 1];
-      f[i] = cm == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(cm - top);
-      if (f[i] != 0.0f) sum = fmaf(f[i], l, sum);
+  for (int i = 0; i < kGatherRows; ++i) {
+    m[i] = -__builtin_inff();
+    sum[i] = 0.0f;
+    o[i] = f32x4{0, 0, 0, 0};
+  }
+#pragma unroll 4
+  for (int g = g0; g <= g1; ++g) {
+    // the first workgroup began the tile, whether or not its share begins with it
+    const int64_t from = ((int64_t)2 * g + (g == g0)) * BM;
+    float cm[kGatherRows], l[kGatherRows];
+    f32x4 v[kGatherRows];
+#pragma unroll
+    for (int i = 0; i < kGatherRows; ++i) {
+      const int64_t p = from + min(first + i * pair, rows - 1);
+      cm[i] = a.stats[2 * p];
+      l[i] = a.stats[2 * p + 1];
       v[i] = f32x4{0, 0, 0, 0};
-      if (4 * lane < a.b.dim) v[i] = *reinterpret_cast<const f32x4 *>(a.part + p * a.b.dim + 4 * lane);
+      if (d < b.dim) v[i] = *reinterpret_cast<const f32x4 *>(a.part + p * b.dim + d);
     }
 #pragma unroll
-    for (int i = 0; i < 4; ++i)
-      if (f[i] != 0.0f) o += v[i] * f[i];
+    for (int i = 0; i < kGatherRows; ++i) {
+      const float top = fmaxf(m[i], cm[i]);
+      const float old = m[i] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m[i] - top);
+      const float now = cm[i] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(cm[i] - top);
+      m[i] = top;
+      sum[i] = fmaf(sum[i], old, l[i] * now);
+      o[i] = o[i] * old + v[i] * now;
+    }
   }
-  const Place place = place_of(a, r, head, r.first + x, -1, top, sum, lane == 0);
-  if (4 * lane < a.b.dim) place.put<E>(4 * lane, o);
+#pragma unroll
+  for (int i = 0; i < kGatherRows; ++i) {
+    if (first + i * pair >= rows) continue;
+    const Place place = place_of(a, r, head, r.first + first + i * pair, -1, m[i], sum[i], d == 0);
+    if (d < b.dim) place.put<E>(d, o[i]);
+  }
 }
 
 // Up to 32 rows: the waves share them and split the keys, each with a place of its

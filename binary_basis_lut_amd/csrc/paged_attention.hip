@@ -22,12 +22,12 @@ constexpr int64_t kChunkRows = 128;
 // Whether equal shares of the key tiles are faster than a workgroup to a row tile
 // and head: `units` key tiles that every row tile has, `busy` of these, in the times
 // of a key tile measured with one workgroup to a CU and with all that it holds.
-// Counting the shares and joining their parts takes about kJoin.  With 128
-// dimensions, 8 key heads of 8: 517 new tokens over 31000 (264 row tiles and heads) 615
-// us by shares, 822 without; 100 over 30000 108 and 590; 256 over 2000 58 and 56; 512
-// over 4000 120 and 102; without cached tokens, where the first row tiles are short and
-// a share has many, 2000 new 122 and 58.
-constexpr double kJoin = 35.0;  // us
+// Counting the shares and joining their parts takes about kJoin.  With 128 dimensions
+// and 64 heads to 8: 517 new tokens over 31000 (264 row tiles and heads) 590 us by
+// shares, 822 without; 100 over 30000 93 and 590; 256 over 2000 49 and 50; 512 over
+// 4000 109 and 95.  Without cached tokens the first row tiles are short and a share
+// has many (2000 new tokens 122 and 58): only cached ones count.
+constexpr double kJoin = 25.0;  // us
 bool shares_pay(double units, int64_t busy, int64_t shares, int64_t dim) {
   const double alone = dim <= 64 ? 0.8 : dim <= 128 ? 1.4 : 2.6, full = dim <= 64 ? 1.4 : dim <= 128 ? 2.5 : 2.6;
   return units * (busy <= 256 ? alone : 0.8 * full) > units * full * (double)busy / (double)shares + kJoin;
@@ -63,6 +63,9 @@ Plan plan_of(const fluxbin_paged_batch &b, int64_t window) {
   return p;
 }
 
+// Workgroups that join the parts of one row tile and head.
+int64_t gather_blocks(int64_t dim) { return kChunkRows / (4 * kGatherRows * (dim <= 128 ? 2 : 1)); }
+
 size_t before_bytes(const Plan &p) { return p.balanced ? (size_t)cdiv((p.tiles + 1) * 4, 256) * 256 : 0; }
 size_t ws_bytes(const fluxbin_paged_batch &b, const Plan &p) { return before_bytes(p) + (size_t)(p.parts * (b.dim + 2)) * 4; }
 
@@ -75,7 +78,7 @@ void launch(const AttentionArgs &a, const Plan &p, hipStream_t st) {
   } else if (p.balanced) {
     hipLaunchKernelGGL((attention_count_kernel<kChunkRows>), dim3(1), dim3(1024), 0, st, a);
     hipLaunchKernelGGL((attention_balanced_kernel<E, D, 1>), dim3(p.shares), dim3(256), 0, st, a);
-    hipLaunchKernelGGL((attention_gather_kernel<E, kChunkRows>), dim3((unsigned)(p.tiles * a.b.kv_heads * (kChunkRows / 4))), dim3(256), 0, st, a);
+    hipLaunchKernelGGL((attention_gather_kernel<E, kChunkRows>), dim3((unsigned)(p.tiles * a.b.kv_heads * gather_blocks(a.b.dim))), dim3(256), 0, st, a);
   } else {
     hipLaunchKernelGGL((attention_chunk_kernel<E, D, 1>), grid, dim3(256), 0, st, a);
   }
@@ -114,7 +117,7 @@ fluxbin_status fluxbin_paged_attention(const fluxbin_paged_batch *batch, const v
   if ((st = check_rows("out", out, ldo, (int64_t)b.heads * b.dim))) return st;
   if (!aligned(lse, 4)) return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "lse is not aligned to its elements");
   const Plan p = plan_of(b, window);
-  const int64_t grid = p.tiles * b.kv_heads * std::max<int64_t>(p.splits, p.balanced ? kChunkRows / 4 : 1);
+  const int64_t grid = p.tiles * b.kv_heads * std::max<int64_t>(p.splits, p.balanced ? gather_blocks(b.dim) : 1);
   if (grid > kMaxGrid) return fail(FLUXBIN_ERR_UNSUPPORTED, "%lld workgroups are beyond one launch", (long long)grid);
   const size_t need = ws_bytes(b, p);
   if (need && (!workspace || workspace_bytes < need))
