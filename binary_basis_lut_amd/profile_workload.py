@@ -52,7 +52,11 @@ profiles/ (each summary names the exact command).  Two modes:
       probabilities), each on distinct operands that pass the 256 MB Infinity
       Cache (at most 16 sets of them), as a HIP graph replayed `reps` times:
       time per call, and the rates of the bytes and operations that the call
-      cannot do without.
+      cannot do without;
+
+  python3 -m binary_basis_lut_amd.profile_workload operators "attend 4096 new" --reps 5
+      cases of perf/more_operators.py by their names (none: all of them), in the
+      same way.
 """
 from __future__ import annotations
 
@@ -392,6 +396,41 @@ def run_int8(args) -> None:
         torch.cuda.empty_cache()
 
 
+def run_operators(args) -> None:
+    import importlib.util
+
+    import torch
+
+    path = os.path.join(os.path.dirname(os.path.dirname(os.path.abspath(__file__))), "perf", "more_operators.py")
+    spec = importlib.util.spec_from_file_location("more_operators", path)
+    cases = importlib.util.module_from_spec(spec)
+    spec.loader.exec_module(cases)
+    cases.own = True
+    for case in cases.listed():
+        if args.cases and case["name"] not in args.cases:
+            continue
+        work = cases.work(case)
+        states = [cases.prepare(case, i) for i in range(max(2, min(16, (600 << 20) // work["bytes"] + 1)))]
+        for s in states:
+            cases.run(s)
+        torch.cuda.synchronize()
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            for s in states:
+                cases.run(s)
+        graph.replay()
+        start, stop = _events()
+        start.record()
+        for _ in range(args.reps):
+            graph.replay()
+        stop.record()
+        torch.cuda.synchronize()
+        us = 1e3 * start.elapsed_time(stop) / args.reps / len(states)
+        print(f"{case['name']}: {us:.2f} us, {work['bytes'] / us / 1e6:.2f} TB/s, {work['flops'] / us / 1e6:.0f} TFLOP/s "
+              f"({len(states)} sets of operands)", flush=True)
+        del states, graph
+
+
 def main() -> int:
     ap = argparse.ArgumentParser(description=__doc__, formatter_class=argparse.RawDescriptionHelpFormatter)
     sub = ap.add_subparsers(dest="mode", required=True)
@@ -438,9 +477,12 @@ def main() -> int:
     i8 = sub.add_parser("int8")
     i8.add_argument("cases", nargs="+", metavar="OP:SIZES,TYPE")
     i8.add_argument("--reps", type=int, default=5)
+    op = sub.add_parser("operators")
+    op.add_argument("cases", nargs="*", metavar="NAME")
+    op.add_argument("--reps", type=int, default=5)
     args = ap.parse_args()
     {"gemv": run_gemv, "decompose": run_decompose, "dense": run_dense, "copy": run_copy, "stream": run_stream,
-     "empty": run_empty, "lookup": run_lookup, "int8": run_int8}[args.mode](args)
+     "empty": run_empty, "lookup": run_lookup, "int8": run_int8, "operators": run_operators}[args.mode](args)
     return 0
 
 
