@@ -85,8 +85,8 @@ __device__ __forceinline__ void forbid(FloatUnit &u, uint32_t bits) {
 // large as the LDS lets two workgroups of 1024 threads be on a CU: 16384 tokens'
 // words, or 8192 with their biases.  Against 256 threads and 4096 tokens
 // throughout, 64 x 131072 bf16 with 4000 tokens of history and 50 biases takes
-// 12.9 us for 15.4, 2048 x 32000 fp32 84 for 99 (6.4 TB/s), one row of 32000 4.7 for
-// 5.8.
+// 12.9 us for 15.4, 2048 x 32000 fp32 84 for 99 and one row of 32000 4.7 for 5.8, each
+// on the same operands again; on others 16, 100 to 106 (5.1 to 5.3 TB/s) and 4.3.
 template <typename E, bool BIAS, bool TINY, int T, int SLICE>
 __global__ __launch_bounds__(T) void adjust_logits_kernel(const AdjustArgs a) {
   typedef typename E::raw raw;

@@ -708,7 +708,7 @@ __global__ __launch_bounds__(256, kChunksPerCu<D>) void attention_balanced_kerne
 
 // The parts of the row tiles that several workgroups had, joined.  A wave has two
 // rows, or two pairs of them where half its lanes hold a row, and loads four parts of
-// each at once (a row to a wave takes 22 us instead of 12 for 4136 rows of 8 heads:
+// each at once (a row to a wave takes 22 us instead of 13 for 4136 rows of 8 heads:
 // each wave looks its tile up before it loads).
 constexpr int kGatherRows = 2;
 template <typename E, int BM>

@@ -79,12 +79,16 @@ class LogitRules:
         self.total_len.zero_()
 
     def append(self, tokens) -> None:
-        """tokens: int64 [max_rows][n] behind each row's history (its last place is written again once it is full)."""
+        """tokens: int64 [max_rows][n] behind each row's history, whose last place holds the latest token once it is full."""
         import torch
 
-        n = tokens.shape[1]
+        n, last = tokens.shape[1], self.max_history - 1
+        _check("tokens", tokens, torch.int64, self.history.device, (self.max_rows, n))
+        if n == 0 or last < 0:
+            return
         at = self.total_len[:, None] + torch.arange(n, device=self.device)
-        self.history.scatter_(1, at.clamp(max=self.max_history - 1), tokens.to(torch.int32))
+        # all that is written to the last place is the latest token, so the order of the writes does not show
+        self.history.scatter_(1, at.clamp(max=last), torch.where(at < last, tokens, tokens[:, -1:]).to(torch.int32))
         self.total_len.add_(n).clamp_(max=self.max_history)
 
     def apply(self, logits, ld: int, dtype: int, rows: int, F) -> None:

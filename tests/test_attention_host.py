@@ -42,12 +42,10 @@ BATCHES = [
 @pytest.mark.parametrize("kw,status", BATCHES)
 def test_batches_that_are_refused(fb, kw, status):
     b = fb.PagedBatch(**L.batch(**kw))
-    ld = 8 * 128
     refused(fb, "fluxbin_paged_attention", [ctypes.byref(b), A, 1 << 20, 0.1, 0, A, 1 << 20, None, A, 72 << 20, None], status)
     refused(fb, "fluxbin_rope_append", [ctypes.byref(b), A, 1 << 20, A, 1 << 20, A, 1 << 20, None, None, 0.0, A, 0, 0, 1.0, None, A, 1 << 20,
                                         None], status)
     refused(fb, "fluxbin_paged_attention_workspace_size", [ctypes.byref(b), ctypes.byref(ctypes.c_size_t())], status)
-    assert ld
 
 
 def attention_args(fb, **kw):
@@ -352,3 +350,25 @@ def test_rules_stand_between_the_head_and_the_scores(calls):
         with pytest.raises(ValueError, match="rules"):
             head.score(cuda(3, 512), cuda(3, 512), cuda(3, dtype=torch.int64), rules=bad)
     assert not calls
+
+
+def test_a_history_that_is_full_keeps_the_latest_token():
+    r = rules(max_rows=2, max_history=5, device="cpu:0")
+    new = lambda *t: torch.tensor([t, [x + 100 for x in t]])
+    r.append(new(1, 2, 3))
+    r.append(new(4))
+    assert r.history.tolist() == [[1, 2, 3, 4, -1], [101, 102, 103, 104, -1]] and r.total_len.tolist() == [4, 4]
+    r.append(new(5, 6, 7))
+    assert r.history.tolist() == [[1, 2, 3, 4, 7], [101, 102, 103, 104, 107]] and r.total_len.tolist() == [5, 5]
+    r.append(new(8))
+    r.append(torch.zeros(2, 0, dtype=torch.int64))
+    assert r.history.tolist() == [[1, 2, 3, 4, 8], [101, 102, 103, 104, 108]] and r.total_len.tolist() == [5, 5]
+    for bad in (torch.zeros(1, 1, dtype=torch.int64), torch.zeros(2, 1, dtype=torch.int32)):
+        with pytest.raises(ValueError, match="tokens"):
+            r.append(bad)
+
+
+def test_no_history_takes_no_tokens():
+    r = rules(max_rows=2, max_history=0, device="cpu:0")
+    r.append(torch.ones(2, 3, dtype=torch.int64))
+    assert r.history.shape == (2, 0) and r.total_len.tolist() == [0, 0]
