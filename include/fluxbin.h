@@ -30,6 +30,11 @@
  * compact columns S, with x[S] gathered at run time (Virtual Columnar
  * Mapping, same summary, section 3 bullet "Virtual Columnar Mapping").
  *
+ * Beside the product stand operators for the rest of such a model's step: the
+ * 8-bit operators (norm, quantisation, int8 product, token scores) and the
+ * attention operators (rotation and append to a paged cache, attention over
+ * it, adjusted logits), each in a section of its own below.
+ *
  * Conventions of every entry point
  *   - All pointers to array data are DEVICE pointers (hipMalloc or torch
  *     CUDA tensors), unless the comment says otherwise.  The caller owns all
@@ -92,7 +97,7 @@ typedef enum {
 } fluxbin_table_precision;
 
 /* Element kinds: the first three for fluxbin_vcm_gather; FLUXBIN_DT_F16, _BF16
- * and _F32 for the activations, outputs and logits of the 8-bit operators. */
+ * and _F32 for the activations, outputs and logits of the other operators. */
 typedef enum {
   FLUXBIN_DT_I8 = 0,   /* int8 elements, [rows][cols] */
   FLUXBIN_DT_F16 = 1,  /* fp16 elements, [rows][cols] */

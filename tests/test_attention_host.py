@@ -95,6 +95,11 @@ def test_rope_append_refuses(fb, kw, status):
     refused(fb, "fluxbin_rope_append", append_args(fb, **kw), status)
 
 
+def test_appending_in_place_with_another_stride_is_refused(fb):
+    for q, ldq, ldqo in ((A, 1024, 1032), (A, 2048, 1024)):
+        refused(fb, "fluxbin_rope_append", append_args(fb, q=q, ldq=ldq, q_out=q, ldqo=ldqo), 1)
+
+
 def adjust_args(**kw):
     d = dict(logits=A, ld=1000, dtype=1, rows=4, vocab=1000, history=A, ldh=50, history_cols=50, prompt_len=A, total_len=A, repetition=A,
              frequency=A, presence=A, bias_index=A, bias_value=A, ldb=8, biases=8, mask=A, ldm=32, out=2 * A, ldo=1000, stream=None)
