@@ -105,6 +105,51 @@ def test_lengths_that_the_host_does_not_know_of(fb):
             check(fb, Paged("f16", 4, 2, 64, 16, lengths, seed=max_kv, max_kv_len=max_kv, table_extra=100))
 
 
+def mixed(seqs, seed, longest):
+    """Sequences without a new token, with one, with a few, and one of them with `longest`."""
+    rng = np.random.default_rng(seed)
+    lengths = [(int(n), int(p)) for n, p in zip(rng.choice([0, 1, 1, 1, 2, 3], seqs), rng.integers(0, 70, seqs))]
+    lengths[int(rng.integers(seqs))] = (longest, 50)
+    return lengths
+
+
+@pytest.mark.parametrize("seqs", [63, 64, 65, 200, 4200])
+def test_many_sequences(fb, seqs):
+    """One round of look-ups and several; single tokens beside a long chunk, in both forms; rows behind the last."""
+    cases = [("single", 2, [(1, s % 40) for s in range(seqs)]), ("mixed", 2, mixed(seqs, seqs, 100))]
+    if seqs <= 200:  # 8 rows to a token, and more than 32 to a sequence
+        cases.append(("chunks", 8, mixed(seqs, seqs + 1, 4 * seqs)))
+    for name, heads, lengths in cases:
+        note(f"{seqs} sequences, {name}")
+        c = Paged("f16", heads, 1, 64, 16, lengths, seed=seqs, behind=0 if name == "single" else 3)
+        whole = {id(t): f64(t) for t in (c.k, c.v)}
+        c.cached = lambda cache, s, c=c, whole=whole: np.array(
+            [whole[id(cache)][c.table_host[s, j // 16], :, j % 16] for j in range(c.lens_host[s])]).reshape(-1, 1, 64)
+        check(fb, c)
+
+
+@pytest.mark.parametrize("seqs", [63, 64, 65, 200, 4200])
+def test_rope_append_of_many_sequences(fb, seqs):
+    """Keys and values as they are, without a rotation, each at its place; the queries too."""
+    for lengths in ([(1, s % 40) for s in range(seqs)], mixed(seqs, seqs, 100)):
+        note(f"rope_append, {seqs} sequences, {sum(n for n, _ in lengths)} rows")
+        c = Paged("bf16", 2, 1, 64, 16, lengths, seed=seqs, behind=3 if max(lengths)[0] > 1 else 0)
+        b = c.upload(fb)
+        x = c.randn(c.tokens, 256)
+        xd, q_out = x.cuda(), torch.full((c.tokens, 128), 7.0, dtype=torch.bfloat16, device="cuda")
+        fb.fluxbin_rope_append(b, xd, 256, xd[:, 128:], 256, xd[:, 192:], 256, None, None, 0.0, None, 0, 0, 1.0, None, q_out, 128)
+        torch.cuda.synchronize()
+        assert torch.equal(q_out[:c.rows].cpu(), x[:c.rows, :128]) and (q_out[c.rows:] == 7).all()
+        want_k, want_v = c.k.clone(), c.v.clone()
+        row = 0
+        for s, (n, past) in enumerate(lengths):
+            for t in range(past, past + n):
+                page = c.table_host[s, t // 16]
+                want_k[page, 0, t % 16], want_v[page, 0, t % 16] = x[row, 128:192], x[row, 192:]
+                row += 1
+        assert torch.equal(c.dev["k"].cpu(), want_k) and torch.equal(c.dev["v"].cpu(), want_v)
+
+
 @pytest.mark.parametrize("window", [1, 2, 31, 100, 1000])
 @pytest.mark.parametrize("dim", [64, 128, 256])
 def test_windows(fb, window, dim):
