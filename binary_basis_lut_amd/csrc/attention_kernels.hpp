@@ -908,7 +908,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttentionArgs
     f32x4 o{0, 0, 0, 0};
     const float top = wave_reduce<MaxF>(cm);
     const float f = cm == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(cm - top);
-    const float sum = wave_reduce<SumF>(f == 0.0f ? 0.0f : f * l);
+    const float sum = wave_reduce<SumF>(f * l);  // a split without keys has l = 0; one whose l is NaN counts whatever its cm
     const float *part = a.part + first * a.b.dim + 4 * lane;
     for (int base = 0; base < a.splits; base += 8) {
       f32x4 v[8];

@@ -1,0 +1,78 @@
+"""fluxbin_paged_attention where scores or values are not numbers, infinite or at the ends of fp32: every division of the keys
+gives what the definition gives (tests/attention_cases.py)."""
+import math
+
+import numpy as np
+import pytest
+
+pytestmark = pytest.mark.gpu
+
+torch = pytest.importorskip("torch")
+
+from tests.attention_cases import U, Paged, attention_bounds, attention_oracle  # noqa: E402
+from tests.test_gpu_attention_ops import attend, balanced, fb, note  # noqa: E402,F401
+
+# how the keys are divided: rows of single tokens in one workgroup or over several, rows of a chunk in one or in shares
+FORMS = ["whole", "splits", "chunk", "shares"]
+
+
+def make(form, dt, dim=128, heads=4, seed=0, past=None):
+    if form in ("whole", "splits"):
+        return Paged(dt, heads, 1, dim, 16, [(1, past or 5000), (3, past or 2000)], seed=seed, decode=False,
+                     max_kv_len={"whole": 1, "splits": 8192}[form])
+    lengths = [(130, past or 1500)]
+    return Paged(dt, heads, 1, dim, 16, lengths, seed=seed, decode=False, max_kv_len=1) if form == "chunk" else \
+        balanced(dt, dim, heads, 1, lengths, seed)
+
+
+def workspace_of(fb, c):
+    return fb.fluxbin_paged_attention_workspace_size(c.upload(fb))
+
+
+def keys(c, s, js):
+    """Key and value rows [dim] of the places js of sequence s, as (page, place in it)."""
+    return [(c.table_host[s, j // c.page], j % c.page) for j in js]
+
+
+def same_as(got, ls, out, lse, tol, tol_lse):
+    """Equal infinities, NaN for NaN, and finite numbers within the tolerance."""
+    for g, w, t in ((got, out, tol), (ls, lse, tol_lse + 4 * U * np.abs(lse))):
+        fine = np.isfinite(w)
+        assert np.array_equal(np.isnan(g), np.isnan(w)), np.argwhere(np.isnan(g) != np.isnan(w))[:5]
+        assert np.array_equal(g[np.isinf(w)], w[np.isinf(w)])
+        assert (np.abs(g[fine] - w[fine]) <= t[fine]).all()
+
+
+@pytest.mark.parametrize("what", ["query", "all of a split", "one key", "one key of small scores", "infinity", "minus infinity"])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("form", FORMS)
+def test_scores_that_are_not_numbers(fb, form, dt, what):
+    note(f"{what}, {form} {dt}")
+    c = make(form, dt)
+    assert (workspace_of(fb, c) > 0) == (form in ("splits", "shares"))
+    scale = 0.05
+    seqs = range(len(c.lengths))
+    if what in ("infinity", "minus infinity", "one key of small scores"):
+        c.q.abs_()
+    if what == "one key of small scores":  # 1/2 or less each times -64: far below the others, and a weight of 0 beside theirs
+        scale = 1.0
+        c.k.mul_(0.01)
+        c.q.clamp_(min=0.25, max=0.5)
+        for s in seqs:
+            for p, i in keys(c, s, range(512, 1024)):
+                c.k[p, :, i] = -16
+    _, _, mag, work, seen = attention_oracle(c, scale)
+    if what == "query":
+        c.q[0, c.dim + 5] = math.nan
+    elif what == "all of a split":
+        for p, i in keys(c, 0, range(512, 1024)):
+            c.k[p, :, i] = math.nan
+    else:
+        p, i = keys(c, 0, [700])[0]
+        c.k[p, 0, i, 9] = {"i": math.inf, "m": -math.inf}.get(what[0], math.nan)
+    out, lse, *_ = attention_oracle(c, scale)
+    assert np.isnan(out).any() == (what != "minus infinity")
+    tol, tol_lse = attention_bounds(c, np.nan_to_num(out), mag, work, seen)
+    got, ls = attend(fb, c, scale)
+    # without the key of weight p the others weigh 1 / (1 - p) times as much, p being less than 1/2
+    same_as(got, ls, out, lse, 2 * tol, 2 * tol_lse)
