@@ -23,7 +23,7 @@ SOURCES = [CSRC / "fluxbin.hip"] + [CSRC / f"gemv_g{g}_rs{rs}_t{t}.hip" for g in
 HEADERS = [CSRC / "common.hpp", CSRC / "gemv_kernel.hpp", CSRC / "gemv_banked.hpp", CSRC / "aux_kernels.hpp",
            CSRC / "decomp_kernels.hpp", CSRC / "probes.hpp", CSRC / "status.hpp", CSRC / "elements.hpp",
            CSRC / "wave_ops.hpp", CSRC / "lds_loads.hpp", CSRC / "paged_batch.hpp", CSRC / "rope_kernels.hpp",
-           CSRC / "adjust_kernels.hpp", CSRC / "attention_kernels.hpp",
+           CSRC / "adjust_kernels.hpp", CSRC / "attention_kernels.hpp", CSRC / "key_weight.hpp",
            CSRC / "act_kernels.hpp", CSRC / "gemm_w8a8_kernel.hpp", CSRC / "logprob_kernels.hpp", ROOT / "include" / "fluxbin.h"]
 DEPS = SOURCES + HEADERS
 BUILD = PKG / "_build"

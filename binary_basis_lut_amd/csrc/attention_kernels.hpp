@@ -30,6 +30,7 @@
 #pragma once
 
 #include "elements.hpp"
+#include "key_weight.hpp"
 #include "lds_loads.hpp"
 #include "paged_batch.hpp"
 #include "wave_ops.hpp"
@@ -56,7 +57,7 @@ struct AttentionArgs {
   float c;
 };
 
-constexpr float kWeightShift = 7.0f, kSlack = 8.0f;
+constexpr float kSlack = 8.0f;
 
 template <typename E>
 __device__ __forceinline__ f32x16 multiply(u32x4 a, u32x4 b, f32x16 acc);
@@ -451,8 +452,8 @@ __device__ __forceinline__ void rows_one_by_one(const AttentionArgs &a, const Ro
       const int key = base + lane;
       int page = -1;
       if (key < k1 && key <= p) page = page_of(b, r.seq, key);
-      const int64_t at = (int64_t)page * b.page_stride + (int64_t)head * b.head_stride +
-                         (int64_t)(key & ((1 << b.page_shift) - 1)) * b.token_stride;
+      const int64_t at = page < 0 ? 0 : (int64_t)page * b.page_stride + (int64_t)head * b.head_stride +
+                                            (int64_t)(key & ((1 << b.page_shift) - 1)) * b.token_stride;
       float s = -__builtin_inff();
       if (page >= 0) {
         s = 0.0f;
@@ -469,7 +470,7 @@ __device__ __forceinline__ void rows_one_by_one(const AttentionArgs &a, const Ro
       if (top == -__builtin_inff()) continue;
       const float factor = __builtin_amdgcn_exp2f((m - top) * a.c);
       m = top;
-      const float w = __builtin_amdgcn_exp2f(fmaf(s, a.c, kWeightShift - m * a.c));
+      const float w = key_weight(page >= 0, s, m, a.c);
       l = fmaf(l, factor, wave_reduce<SumF>(w));
       o *= factor;
       for (int j0 = 0; j0 < 64; j0 += 8) {
