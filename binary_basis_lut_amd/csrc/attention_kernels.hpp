@@ -50,7 +50,7 @@ struct AttentionArgs {
   const uint16_t *q;
   uint16_t *out;
   float *lse;      // may be null
-  float *part, *stats;  // parts of rows: o [part][dim], (c m, l) [part]
+  float *part, *stats;  // parts of rows: o [part][dim], (m, l) [part]
   int32_t *before;      // balanced: key tiles of the row tiles before each, and of all of them
   int64_t ldq, ldo;
   int32_t group, window, splits, tiles, workgroups;
@@ -382,9 +382,12 @@ struct WaveTile {
   }
 
   // Whether an infinity or NaN has come into o: one among the values, which a weight
-  // of 0 turns into NaN for rows that do not see it, or one among the scores.
-  __device__ __forceinline__ bool unclean() const {
+  // of 0 turns into NaN for rows that do not see it, or one among the scores; or
+  // whether c m has left fp32's range, where the weights were not what they should be.
+  __device__ __forceinline__ bool unclean(float c) const {
     float z = 0.0f;
+#pragma unroll
+    for (int x = 0; x < QB; ++x) z = m[x] == -__builtin_inff() ? z : fmaf(m[x] * c, 0.0f, z);
 #pragma unroll
     for (int i = 0; i < DB; ++i)
 #pragma unroll
@@ -396,8 +399,9 @@ struct WaveTile {
 };
 
 // What a row comes to: its output and lse, or the part of a split.
-__device__ __forceinline__ float lse_of(float cm, float l) {
-  return l == 0.0f ? -__builtin_inff() : 0.69314718055994530942f * (cm - kWeightShift + log2f(l));
+__device__ __forceinline__ float lse_of(float m, float c, float l) {
+  const float ln2 = 0.69314718055994530942f;  // before c, so that nothing passes lse itself
+  return l == 0.0f ? -__builtin_inff() : fmaf(ln2 * m, c, ln2 * (log2f(l) - kWeightShift));
 }
 struct Place {
   uint16_t *out;
@@ -411,19 +415,19 @@ struct Place {
 };
 
 // Where a row's o goes: the output, or its part number `index` (< 0: none).  The
-// row's lse, or the part's (c m, l), is written here by the lane that is `first` of
+// row's lse, or the part's (m, l), is written here by the lane that is `first` of
 // those that have the row.
-__device__ __forceinline__ Place place_of(const AttentionArgs &a, const Rows &r, int head, int row, int64_t index, float cm, float l, bool first) {
+__device__ __forceinline__ Place place_of(const AttentionArgs &a, const Rows &r, int head, int row, int64_t index, float m, float l, bool first) {
   const int token = r.start + row / a.group, h = head * a.group + row % a.group;
   Place p;
   p.out = a.out + (int64_t)token * a.ldo + h * a.b.dim;
   p.part = index >= 0 ? a.part + index * a.b.dim : nullptr;
   p.inv = l == 0.0f ? 0.0f : 1.0f / l;
   if (first && index >= 0) {
-    a.stats[2 * index] = cm;
+    a.stats[2 * index] = m;
     a.stats[2 * index + 1] = l;
   } else if (first && a.lse) {
-    a.lse[(int64_t)token * a.b.heads + h] = lse_of(cm, l);
+    a.lse[(int64_t)token * a.b.heads + h] = lse_of(m, a.c, l);
   }
   return p;
 }
@@ -491,7 +495,7 @@ __device__ __forceinline__ void rows_one_by_one(const AttentionArgs &a, const Ro
           }
       }
     }
-    const Place place = place_of(a, r, head, row, parts.of(row - r.first), m * a.c, l, lane == 0);
+    const Place place = place_of(a, r, head, row, parts.of(row - r.first), m, l, lane == 0);
     if (4 * lane < b.dim) place.put<E>(4 * lane, o);
   }
 }
@@ -568,7 +572,7 @@ __device__ __forceinline__ void attend_rows(const AttentionArgs &a, const Rows &
     w.add_values(lds.tile[buf][1], lane, p);
     __builtin_amdgcn_s_setprio(1);
   }
-  if (w.unclean()) {
+  if (w.unclean(a.c)) {
     rows_one_by_one<E>(a, r, head, parts, first_row, end_row, 1, t0 * KT, t1 * KT, lane);
     return;
   }
@@ -577,7 +581,7 @@ __device__ __forceinline__ void attend_rows(const AttentionArgs &a, const Rows &
     const int row = first_row + 32 * x + lane % 32;
     const float l = other_half_sum(w.l[x]);
     if (row >= end_row) continue;
-    const Place place = place_of(a, r, head, row, parts.of(row - r.first), w.m[x] * a.c, l, lane < 32);
+    const Place place = place_of(a, r, head, row, parts.of(row - r.first), w.m[x], l, lane < 32);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -737,21 +741,21 @@ __global__ __launch_bounds__(256) void attention_gather_kernel(const AttentionAr
   for (int g = g0; g <= g1; ++g) {
     // the first workgroup began the tile, whether or not its share begins with it
     const int64_t from = ((int64_t)2 * g + (g == g0)) * BM;
-    float cm[kGatherRows], l[kGatherRows];
+    float now_m[kGatherRows], l[kGatherRows];
     f32x4 v[kGatherRows];
 #pragma unroll
     for (int i = 0; i < kGatherRows; ++i) {
       const int64_t p = from + min(first + i * pair, rows - 1);
-      cm[i] = a.stats[2 * p];
+      now_m[i] = a.stats[2 * p];
       l[i] = a.stats[2 * p + 1];
       v[i] = f32x4{0, 0, 0, 0};
       if (d < b.dim) v[i] = *reinterpret_cast<const f32x4 *>(a.part + p * b.dim + d);
     }
 #pragma unroll
     for (int i = 0; i < kGatherRows; ++i) {
-      const float top = fmaxf(m[i], cm[i]);
-      const float old = m[i] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(m[i] - top);
-      const float now = cm[i] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(cm[i] - top);
+      const float top = fmaxf(m[i], now_m[i]);
+      const float old = m[i] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f((m[i] - top) * a.c);
+      const float now = now_m[i] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f((now_m[i] - top) * a.c);
       m[i] = top;
       sum[i] = fmaf(sum[i], old, l[i] * now);
       o[i] = o[i] * old + v[i] * now;
@@ -849,7 +853,7 @@ __global__ __launch_bounds__(64 * Few<D>::W) void attention_few_kernel(const Att
     stats[0][wave][lane] = w.m[0];
     stats[1][wave][lane] = l;
   }
-  bool bad = w.unclean();
+  bool bad = w.unclean(a.c);
   if (lane == 0) any_bad[wave] = bad;
   __syncthreads();
   const int rows = min(32, r.count - r.first);
@@ -889,7 +893,7 @@ __global__ __launch_bounds__(64 * Few<D>::W) void attention_few_kernel(const Att
       sum = fmaf(stats[1][v][row], __builtin_amdgcn_exp2f((m - big) * a.c), sum);
       o += *reinterpret_cast<const f32x4 *>(sums + (v * 32 + row) * D + sum_at(row, d / 4));
     }
-    place_of(a, r, head, r.first + row, parts.of(row), big * a.c, sum, d == 0).put<E>(d, o);
+    place_of(a, r, head, r.first + row, parts.of(row), big, sum, d == 0).put<E>(d, o);
   }
 }
 
@@ -900,16 +904,16 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttentionArgs
   const Rows r = rows_of<32>(a, tile, lane);
   for (int x = threadIdx.x / 64; x < min(32, r.count - r.first); x += 4) {
     const int64_t first = (int64_t)blockIdx.x * a.splits * 32 + x;
-    float cm = -__builtin_inff(), l = 0.0f;
+    float m = -__builtin_inff(), l = 0.0f;
     if (lane < a.splits) {
-      cm = a.stats[2 * (first + lane * 32)];
+      m = a.stats[2 * (first + lane * 32)];
       l = a.stats[2 * (first + lane * 32) + 1];
     }
     // eight splits' parts are in flight; those of splits without keys hold zeros
     f32x4 o{0, 0, 0, 0};
-    const float top = wave_reduce<MaxF>(cm);
-    const float f = cm == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f(cm - top);
-    const float sum = wave_reduce<SumF>(f * l);  // a split without keys has l = 0; one whose l is NaN counts whatever its cm
+    const float top = wave_reduce<MaxF>(m);
+    const float f = m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f((m - top) * a.c);
+    const float sum = wave_reduce<SumF>(f * l);  // a split without keys has l = 0; one whose l is NaN counts whatever its m
     const float *part = a.part + first * a.b.dim + 4 * lane;
     for (int base = 0; base < a.splits; base += 8) {
       f32x4 v[8];

@@ -22,11 +22,11 @@ FB_BOTH float power_of_two(float x) {
 #endif
 }
 
-// The weight of a key of score s under the maximum m.  One that is not there weighs
-// nothing whatever its s and m are: c m may pass fp32's range, and the difference of
-// two infinities is no weight of 0.
+// The weight of a key of score s under the maximum m.  The difference comes before the
+// product: c s and c m may both pass fp32's range.  A key that is not there weighs
+// nothing whatever s and m are.
 FB_BOTH float key_weight(bool there, float s, float m, float c) {
-  return there ? power_of_two(fmaf(s, c, kWeightShift - m * c)) : 0.0f;
+  return there ? power_of_two(fmaf(s - m, c, kWeightShift)) : 0.0f;
 }
 
 }  // namespace fluxbin

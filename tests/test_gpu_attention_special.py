@@ -76,3 +76,24 @@ def test_scores_that_are_not_numbers(fb, form, dt, what):
     got, ls = attend(fb, c, scale)
     # without the key of weight p the others weigh 1 / (1 - p) times as much, p being less than 1/2
     same_as(got, ls, out, lse, 2 * tol, 2 * tol_lse)
+
+
+@pytest.mark.parametrize("sign", [1, -1])
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("form", FORMS)
+def test_scores_at_the_ends_of_fp32(fb, form, dt, sign):
+    """z = scale q . k of 2.7e38, z log2(e) beyond fp32: the keys of the largest one share the weight."""
+    note(f"scores of {sign} 2.7e38, {form} {dt}")
+    c = make(form, dt, past=1100)
+    workspace_of(fb, c)
+    c.q.zero_()
+    c.q[:, ::c.dim] = 16384
+    for s in range(len(c.lengths)):
+        for j, (p, i) in enumerate(keys(c, s, range(c.lens_host[s]))):
+            c.k[p, 0, i, 0] = sign * (16384, 16512)[(j % 3 == 0) == (sign > 0)]
+    out, lse, mag, work, seen = attention_oracle(c, float(np.float32(1e30)))
+    assert (np.abs(lse) > 2.6e38).all() and (np.abs(lse) < 3e38).all()
+    # the weights are 1 or 0: a product's rounding moves no score past another, so only sums and roundings count in out
+    tol, _ = attention_bounds(c, out, mag, 0 * work, seen)
+    _, tol_lse = attention_bounds(c, out, mag, work, seen)
+    same_as(*attend(fb, c, 1e30), out, lse, tol, tol_lse)

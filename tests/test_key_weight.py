@@ -43,3 +43,18 @@ def test_a_key_that_is_not_there_weighs_nothing(weights):
     """Its score is -inf.  Only a weight other than 0 makes the kernel look for a key's values."""
     m, c = (x.ravel() for x in np.meshgrid(np.concatenate([M, -M, [np.inf]]), C))
     assert (weights(False, -np.inf, m, c) == 0).all()
+
+
+def test_weights_over_all_of_fp32(weights):
+    """2^(c (s - m) + 7): the difference rounds once, its product and the sum once more."""
+    m, d, c = (x.ravel() for x in np.meshgrid(np.concatenate([M, -M]), [0, 1e-38, 1e-30, 1e-20, 0.5, 1, 3, 40, 1e10, 1e38, 3.4e38], C))
+    with np.errstate(all="ignore"):
+        s = (m - d.astype(np.float32)).astype(np.float32)
+    s = np.maximum(s, -np.finfo(np.float32).max)
+    got = weights(True, s, m, c).astype(np.float64)
+    e = np.maximum(c.astype(np.float64) * (s.astype(np.float64) - m.astype(np.float64)) + 7, -2000)  # 2^-2000 is 0
+    want = np.exp2(e)
+    tol = want * (np.exp2(3 * 2.0 ** -24 * (np.abs(e) + 14)) - 1 + 2.0 ** -22) + 2.0 ** -149
+    off = ~(np.abs(got - want) <= tol)
+    assert not off.any(), np.stack([m, s, c, got, want], 1)[off][:5]
+    assert (weights(True, np.float32(-np.inf), m, c) == 0).all()
