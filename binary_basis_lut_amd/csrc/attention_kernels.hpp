@@ -439,10 +439,20 @@ struct Parts {
   __device__ __forceinline__ int64_t of(int x) const { return from < 0 ? -1 : from + x * step; }
 };
 
+// A sum of weighted values times a factor of 0 or more: an infinity or NaN in it, which
+// has a weight above 0 however small, stays when the factor underflows.
+__device__ __forceinline__ f32x4 rescaled(f32x4 o, float factor) {
+#pragma unroll
+  for (int i = 0; i < 4; ++i) o[i] *= fabsf(o[i]) < __builtin_inff() ? factor : 1.0f;
+  return o;
+}
+
 // Rows [from, to) of a workgroup over the keys [k0, k1), one after the other by a
 // wave: 64 keys at a time, a lane to a key, then a lane to four dimensions.  For
 // rows that an infinity or NaN came into: a matrix product carries one to all its
-// rows (0 times infinity); here a key whose weight is 0 is left out.
+// rows (0 times infinity); here a key that a row does not see, or whose score is
+// -inf, is left out, and any other infinite value or NaN counts whatever its weight
+// rounds to, so that neither the keys' order nor their division matters.
 template <typename E>
 __device__ __forceinline__ void rows_one_by_one(const AttentionArgs &a, const Rows &r, int head, const Parts &parts, int from, int to, int step,
                                                 int k0, int k1, int lane) {
@@ -476,7 +486,8 @@ __device__ __forceinline__ void rows_one_by_one(const AttentionArgs &a, const Ro
       m = top;
       const float w = key_weight(page >= 0, s, m, a.c);
       l = fmaf(l, factor, wave_reduce<SumF>(w));
-      o *= factor;
+      o = rescaled(o, factor);
+      const uint64_t counts = __ballot(page >= 0 && s != -__builtin_inff());
       for (int j0 = 0; j0 < 64; j0 += 8) {
         words2 x[8];
         float wj[8];
@@ -485,13 +496,16 @@ __device__ __forceinline__ void rows_one_by_one(const AttentionArgs &a, const Ro
           wj[j] = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, w), j0 + j));
           const int64_t v = (int64_t)__builtin_amdgcn_readlane((int)(at >> 32), j0 + j) << 32 | (uint32_t)__builtin_amdgcn_readlane((int)at, j0 + j);
           x[j] = words2{0, 0};
-          if (wj[j] != 0.0f && 4 * lane < b.dim) x[j] = *reinterpret_cast<const words2 *>(b.v + v + 4 * lane);
+          if ((counts >> (j0 + j) & 1) && 4 * lane < b.dim) x[j] = *reinterpret_cast<const words2 *>(b.v + v + 4 * lane);
         }
 #pragma unroll
         for (int j = 0; j < 8; ++j)
-          if (wj[j] != 0.0f) {
+          if (counts >> (j0 + j) & 1) {
 #pragma unroll
-            for (int i = 0; i < 4; ++i) o[i] = fmaf(wj[j], E::load((uint16_t)(x[j][i / 2] >> (16 * (i % 2)))), o[i]);
+            for (int i = 0; i < 4; ++i) {
+              const float v = E::load((uint16_t)(x[j][i / 2] >> (16 * (i % 2))));
+              o[i] = fmaf(fabsf(v) < __builtin_inff() ? wj[j] : 1.0f, v, o[i]);
+            }
           }
       }
     }
@@ -758,7 +772,7 @@ __global__ __launch_bounds__(256) void attention_gather_kernel(const AttentionAr
       const float now = now_m[i] == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f((now_m[i] - top) * a.c);
       m[i] = top;
       sum[i] = fmaf(sum[i], old, l[i] * now);
-      o[i] = o[i] * old + v[i] * now;
+      o[i] = rescaled(o[i], old) + rescaled(v[i], now);
     }
   }
 #pragma unroll
@@ -925,7 +939,7 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttentionArgs
 #pragma unroll
       for (int i = 0; i < 8; ++i) {
         const float fs = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), (base + i) % 64));
-        if (base + i < a.splits && fs != 0.0f) o += v[i] * fs;
+        if (base + i < a.splits) o += rescaled(v[i], fs);
       }
     }
     const Place place = place_of(a, r, head, r.first + x, -1, top, sum, lane == 0);

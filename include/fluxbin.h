@@ -601,7 +601,9 @@ fluxbin_status fluxbin_rope_append(const fluxbin_paged_batch *batch, const void 
  *   out = sum_J exp(z_j - lse) v_j.
  * A row without any key (or with z = -inf for all of them) has out = 0 and
  * lse = -inf.  Keys outside J take no part, whatever they hold, infinities
- * and NaN too.  lse (fp32 [tokens][heads], natural logarithm) may be NULL; with
+ * and NaN too, nor do keys of z = -inf.  An infinite value or NaN of any other
+ * key shows in its dimension however small its weight, and a row that sees a z
+ * of NaN or +inf is NaN, its lse too.  lse (fp32 [tokens][heads], natural logarithm) may be NULL; with
  * it, parts computed apart can be joined.  scale is positive and at most 1e30;
  * z is meant to stay in fp32's range.
  * Products are taken in dtype's matrix instructions with fp32 sums; the

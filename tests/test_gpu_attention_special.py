@@ -97,3 +97,26 @@ def test_scores_at_the_ends_of_fp32(fb, form, dt, sign):
     tol, _ = attention_bounds(c, out, mag, 0 * work, seen)
     _, tol_lse = attention_bounds(c, out, mag, work, seen)
     same_as(*attend(fb, c, 1e30), out, lse, tol, tol_lse)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("form", FORMS)
+def test_infinite_values_under_vanishing_weights(fb, form, dt):
+    """A weight is positive however small: an infinity shows, whether it comes before the maximum or after it."""
+    note(f"infinities under weights of e^-300, {form} {dt}")
+    c = make(form, dt)
+    workspace_of(fb, c)
+    c.q.fill_(1)
+    c.k.mul_(0.01)
+    n = c.lens_host[0] - c.lengths[0][0]
+    for p, i in keys(c, 0, list(range(64)) + list(range(n - 20, n - 8))):
+        c.k[p, :, i] = -300 / 128
+    _, _, mag, work, seen = attention_oracle(c, 1.0)
+    for j, d, v in ((5, 3, math.inf), (n - 10, 4, -math.inf), (7, 5, math.inf), (n - 12, 5, -math.inf), (9, 6, math.nan), (n - 13, 7, math.nan)):
+        p, i = keys(c, 0, [j])[0]
+        c.v[p, 0, i, d] = v
+    out, lse, *_ = attention_oracle(c, 1.0)
+    row = out[:c.lengths[0][0]]
+    assert (row[..., 3] == math.inf).all() and (row[..., 4] == -math.inf).all() and np.isnan(row[..., 5:8]).all()
+    tol, tol_lse = attention_bounds(c, np.nan_to_num(out, posinf=0, neginf=0), mag, work, seen)
+    same_as(*attend(fb, c, 1.0), out, lse, tol, tol_lse)
