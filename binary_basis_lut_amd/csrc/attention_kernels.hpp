@@ -916,6 +916,7 @@ template <typename E>
 __global__ __launch_bounds__(256) void attention_join_kernel(const AttentionArgs a) {
   const int lane = threadIdx.x % 64, head = blockIdx.x % a.b.kv_heads, tile = blockIdx.x / a.b.kv_heads;
   const Rows r = rows_of<32>(a, tile, lane);
+  if (r.count == 0) return;
   for (int x = threadIdx.x / 64; x < min(32, r.count - r.first); x += 4) {
     const int64_t first = (int64_t)blockIdx.x * a.splits * 32 + x;
     float m = -__builtin_inff(), l = 0.0f;

@@ -534,9 +534,9 @@ fluxbin_status fluxbin_token_logprobs(const void *logits, int64_t ld, int32_t dt
  * Shared rules: those of the 8-bit operators, and
  *   - seqs sequences have new tokens, the rows of q, k, v and out in order:
  *     sequence s has the rows seq_starts[s] .. seq_starts[s + 1] - 1 (int32
- *     [seqs + 1], not decreasing, from 0 on), or row s alone where seq_starts
- *     is NULL (then tokens = seqs: a decode step).  Rows behind the last
- *     sequence are left as they were.
+ *     [seqs + 1], not decreasing, 0 or more), or row s alone where seq_starts
+ *     is NULL (then tokens = seqs: a decode step).  Rows before the first
+ *     sequence and behind the last one are left as they were.
  *   - kv_lens[s] (int32) is the length of s's cache with its new tokens, so
  *     that its i-th of n new tokens has the index t = kv_lens[s] - n + i.
  *   - The cache is cache_pages pages of page_size tokens.  Index t of s is

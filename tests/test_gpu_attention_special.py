@@ -9,7 +9,7 @@ pytestmark = pytest.mark.gpu
 
 torch = pytest.importorskip("torch")
 
-from tests.attention_cases import U, Paged, attention_bounds, attention_oracle  # noqa: E402
+from tests.attention_cases import U, Paged, attention_bounds, attention_oracle, f64  # noqa: E402
 from tests.test_gpu_attention_ops import attend, balanced, fb, note  # noqa: E402,F401
 
 # how the keys are divided: rows of single tokens in one workgroup or over several, rows of a chunk in one or in shares
@@ -120,3 +120,27 @@ def test_infinite_values_under_vanishing_weights(fb, form, dt):
     assert (row[..., 3] == math.inf).all() and (row[..., 4] == -math.inf).all() and np.isnan(row[..., 5:8]).all()
     tol, tol_lse = attention_bounds(c, np.nan_to_num(out, posinf=0, neginf=0), mag, work, seen)
     same_as(*attend(fb, c, 1.0), out, lse, tol, tol_lse)
+
+
+@pytest.mark.parametrize("form", FORMS)
+def test_rows_before_the_first_sequence(fb, form):
+    """They are left as they were, as those behind the last one are."""
+    note(f"rows before the first sequence, {form}")
+    few = form in ("whole", "splits")
+    before, lengths = (9, [(1, 5000), (6, 2000)]) if few else (140, [(130, 1500)])
+    c = Paged("f16", 4, 1, 128, 16, lengths, seed=1, decode=False, max_kv_len={"whole": 1, "splits": 8192, "chunk": 1, "shares": 0}[form],
+              behind=before, table_extra=1 << 16 if form == "shares" else 0)
+    b = c.upload(fb)
+    c.dev["starts"].add_(before)
+    q = torch.zeros_like(c.dev["q"])
+    q[before:] = c.dev["q"][:c.rows]
+    out, ls = torch.full_like(q, 7.0), torch.full((c.tokens, 4), 7.0, device="cuda")
+    need = fb.fluxbin_paged_attention_workspace_size(b)
+    assert (need > 0) == (form in ("splits", "shares"))
+    ws = torch.full((max(need, 16) // 4 + 4,), math.nan, dtype=torch.float32, device="cuda")
+    fb.fluxbin_paged_attention(b, q, 512, 0.1, 0, out, 512, ls, ws, need)
+    torch.cuda.synchronize()
+    assert (out[:before] == 7).all() and (ls[:before] == 7).all()
+    want, lse, mag, work, seen = attention_oracle(c, 0.1)
+    tol, tol_lse = attention_bounds(c, want, mag, work, seen)
+    same_as(f64(out[before:]).reshape(want.shape), f64(ls[before:]), want, lse, tol, tol_lse)
