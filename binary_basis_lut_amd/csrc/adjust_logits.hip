@@ -53,6 +53,8 @@ extern "C" fluxbin_status fluxbin_adjust_logits(const void *logits, int64_t ld, 
   if (ld < vocab || ldo < vocab)
     return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "ld = %lld or ldo = %lld below vocab = %lld", (long long)ld, (long long)ldo, (long long)vocab);
   if (logits == out && ld != ldo) return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "out is logits with another stride");
+  if (logits != out && rows_overlap(logits, ld, out, ldo, rows, vocab, bytes))
+    return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "out overlaps logits without being them");
   if (history_cols && !history) return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "history_cols without history");
   if (history && ldh < history_cols)
     return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "ldh = %lld < history_cols = %lld", (long long)ldh, (long long)history_cols);

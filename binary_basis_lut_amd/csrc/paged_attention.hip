@@ -115,6 +115,8 @@ fluxbin_status fluxbin_paged_attention(const fluxbin_paged_batch *batch, const v
   if (b.tokens == 0 || b.seqs == 0) return ok();
   if ((st = check_rows("q", q, ldq, (int64_t)b.heads * b.dim))) return st;
   if ((st = check_rows("out", out, ldo, (int64_t)b.heads * b.dim))) return st;
+  if ((q != out || ldq != ldo) && rows_overlap(q, ldq, out, ldo, b.tokens, (int64_t)b.heads * b.dim, 2))
+    return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "out overlaps q without being it");
   if (!aligned(lse, 4)) return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "lse is not aligned to its elements");
   const Plan p = plan_of(b, window);
   const int64_t grid = p.tiles * b.kv_heads * std::max<int64_t>(p.splits, p.balanced ? gather_blocks(b.dim) : 1);

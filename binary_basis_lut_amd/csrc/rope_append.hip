@@ -57,6 +57,8 @@ extern "C" fluxbin_status fluxbin_rope_append(const fluxbin_paged_batch *batch, 
   if (q && (st = check_rows("q", q, ldq, (int64_t)b.heads * b.dim))) return st;
   if (q && (st = check_rows("q_out", q_out, ldqo, (int64_t)b.heads * b.dim))) return st;
   if (q && q == q_out && ldq != ldqo) return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "q_out is q with another stride");
+  if (q && q != q_out && rows_overlap(q, ldq, q_out, ldqo, b.tokens, (int64_t)b.heads * b.dim, 2))
+    return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "q_out overlaps q without being it");
   if ((st = check_rows("k", k, ldk, (int64_t)b.kv_heads * b.dim))) return st;
   if ((st = check_rows("v", v, ldv, (int64_t)b.kv_heads * b.dim))) return st;
   if (!aligned(q_norm, 2) || !aligned(k_norm, 2) || !aligned(positions, 4) || !aligned(freq, 8))

@@ -586,7 +586,8 @@ typedef enum { FLUXBIN_ROPE_HALF = 0, FLUXBIN_ROPE_NEAR = 1 } fluxbin_rope_pairs
  * it a long context asks for; angles are taken in 64 bits, the rest is fp32,
  * rounded once.  rotary_dim: a multiple of 8 in [0, dim]; 0 rotates nothing
  * (freq may be NULL).  rope_scale multiplies the rotated elements only.
- * q may be NULL (keys and values alone), q_out may be q with the same stride.
+ * q may be NULL (keys and values alone); q_out may be q with the same stride,
+ * or not overlap it, and overlaps neither k nor v.
  * Queries of a token whose page is not there are written all the same.  A
  * head whose sum of squares is not finite in fp32 becomes NaN. */
 fluxbin_status fluxbin_rope_append(const fluxbin_paged_batch *batch, const void *q, int64_t ldq, const void *k, int64_t ldk,
@@ -611,7 +612,7 @@ fluxbin_status fluxbin_rope_append(const fluxbin_paged_batch *batch, const void 
  * dtype for the second (where sequences have few rows, in two parts).  Rows that
  * share a workgroup with an infinite or NaN key or value are computed again one
  * by one, slowly.  bf16 values beyond 2^100 overflow the sums.
- * out may not overlap q.  workspace: at least
+ * out may be q with the same stride, or not overlap it.  workspace: at least
  * fluxbin_paged_attention_workspace_size() bytes (never above 72 MiB), 16-byte
  * aligned, free for other use once the call's work has finished; NULL where
  * that size is 0.  One call at a time per workspace: graphs that share one are

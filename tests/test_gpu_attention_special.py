@@ -144,3 +144,27 @@ def test_rows_before_the_first_sequence(fb, form):
     want, lse, mag, work, seen = attention_oracle(c, 0.1)
     tol, tol_lse = attention_bounds(c, want, mag, work, seen)
     same_as(f64(out[before:]).reshape(want.shape), f64(ls[before:]), want, lse, tol, tol_lse)
+
+
+@pytest.mark.parametrize("dt", ["f16", "bf16"])
+@pytest.mark.parametrize("form", FORMS)
+def test_outputs_over_the_queries(fb, form, dt):
+    """The same bits as apart, also where rows are computed key by key and read their query again."""
+    note(f"out is q, {form} {dt}")
+    for bad in (False, True):
+        c = make(form, dt, seed=2)
+        if bad:
+            p, i = keys(c, 0, [100])[0]
+            c.v[p, 0, i, 9] = math.inf
+        b = c.upload(fb)
+        need = fb.fluxbin_paged_attention_workspace_size(b)
+        ws = torch.empty(max(need, 16), dtype=torch.uint8, device="cuda")
+        ld = c.heads * c.dim + 8
+        q = torch.full((c.tokens, ld), 7.0, dtype=c.dev["q"].dtype, device="cuda")
+        q[:, :-8] = c.dev["q"]
+        apart = torch.full_like(q, 7.0)
+        for out in (apart, q):
+            fb.fluxbin_paged_attention(b, q, ld, 0.1, 0, out, ld, None, ws, need)
+        torch.cuda.synchronize()
+        assert torch.isinf(apart).any() == bad
+        assert torch.equal(q, apart)
