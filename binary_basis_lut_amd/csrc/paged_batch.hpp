@@ -63,6 +63,9 @@ __device__ __forceinline__ int page_of(const Paged &b, int s, int index) {
   return (uint32_t)p < (uint32_t)b.pages ? p : -1;
 }
 
+// Keys of a sequence: the kernels look up to a few hundred beyond the last one, in 32 bits.
+constexpr int64_t kMostKeys = ((int64_t)1 << 31) - (1 << 16);
+
 inline fluxbin_status check_paged(const fluxbin_paged_batch *b) {
   if (!b) return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "batch is NULL");
   if (b->abi_version != FLUXBIN_ABI_VERSION)
@@ -86,8 +89,8 @@ inline fluxbin_status check_paged(const fluxbin_paged_batch *b) {
   if (b->max_kv_len < 0) return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "max_kv_len = %lld", (long long)b->max_kv_len);
   if (b->table_pages < 0 || b->table_ld < b->table_pages)
     return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "table_pages = %lld, table_ld = %lld", (long long)b->table_pages, (long long)b->table_ld);
-  if (b->table_pages > ((int64_t)1 << 31) / b->page_size - 1)
-    return fail(FLUXBIN_ERR_UNSUPPORTED, "table_pages * page_size reaches 2^31");
+  if (b->table_pages > kMostKeys / b->page_size)
+    return fail(FLUXBIN_ERR_UNSUPPORTED, "table_pages * page_size above 2^31 - 2^16");
   if (b->cache_pages < 0) return fail(FLUXBIN_ERR_INVALID_ARGUMENT, "cache_pages = %lld", (long long)b->cache_pages);
   if (b->cache_pages >= (int64_t)1 << 31) return fail(FLUXBIN_ERR_UNSUPPORTED, "cache_pages reaches 2^31");
   if (b->page_stride < 0 || b->head_stride < 0 || b->page_stride % 8 || b->head_stride % 8 || b->token_stride % 8)

@@ -565,7 +565,7 @@ typedef struct {
   int64_t max_kv_len;            /* what no kv_lens[s] passes (0: table_pages * page_size).  It decides how the
                                     work is divided, not what is computed */
   const int32_t *seq_starts, *kv_lens, *page_table;
-  int64_t table_ld, table_pages; /* table_ld at least table_pages; table_pages * page_size below 2^31 */
+  int64_t table_ld, table_pages; /* table_ld at least table_pages; table_pages * page_size at most 2^31 - 2^16 */
   void *k_cache, *v_cache;       /* 16-byte aligned */
   int64_t cache_pages, page_stride, head_stride, token_stride; /* multiples of 8; token_stride dim .. 2^24 */
 } fluxbin_paged_batch;
