@@ -11,8 +11,8 @@
 // is the fp32 sum of the weights before that.  That rounding of every weight adds
 // about as much to an output's error as the output's own (in quadrature); a chunk's
 // products are what bounds it and bear no more, single tokens wait for memory and
-// take a second product with what the rounding left.  Two sets of keys are joined by moving both to the larger m, so keys
-// may be split over waves and workgroups.
+// take a second product with what the rounding left.  Two sets of keys are joined by
+// moving both to the larger m, so keys may be split over waves and workgroups.
 //
 // All rows that read one key head are rows of one matrix: row r of a sequence is
 // query head r % G of its group of G and token r / G.  Both products run
@@ -432,12 +432,9 @@ __device__ __forceinline__ Place place_of(const AttentionArgs &a, const Rows &r,
   return p;
 }
 
-// Which parts the rows of a workgroup write: row x of them is part `from` + x `step`
-// (from < 0: none, the rows are whole).
-struct Parts {
-  int64_t from, step;
-  __device__ __forceinline__ int64_t of(int x) const { return from < 0 ? -1 : from + x * step; }
-};
+// The part that row x of a workgroup writes, where its first row writes part `parts`
+// (< 0: none, the rows are whole).
+__device__ __forceinline__ int64_t part_of(int64_t parts, int x) { return parts < 0 ? -1 : parts + x; }
 
 // A sum of weighted values times a factor of 0 or more: an infinity or NaN in it, which
 // has a weight above 0 however small, stays when the factor underflows.
@@ -454,7 +451,7 @@ __device__ __forceinline__ f32x4 rescaled(f32x4 o, float factor) {
 // -inf, is left out, and any other infinite value or NaN counts whatever its weight
 // rounds to, so that neither the keys' order nor their division matters.
 template <typename E>
-__device__ __forceinline__ void rows_one_by_one(const AttentionArgs &a, const Rows &r, int head, const Parts &parts, int from, int to, int step,
+__device__ __forceinline__ void rows_one_by_one(const AttentionArgs &a, const Rows &r, int head, int64_t parts, int from, int to, int step,
                                                 int k0, int k1, int lane) {
   const Paged &b = a.b;
   for (int row = from; row < to; row += step) {
@@ -509,7 +506,7 @@ __device__ __forceinline__ void rows_one_by_one(const AttentionArgs &a, const Ro
           }
       }
     }
-    const Place place = place_of(a, r, head, row, parts.of(row - r.first), m, l, lane == 0);
+    const Place place = place_of(a, r, head, row, part_of(parts, row - r.first), m, l, lane == 0);
     if (4 * lane < b.dim) place.put<E>(4 * lane, o);
   }
 }
@@ -529,7 +526,7 @@ struct ChunkTiles {
 // while one is worked on.
 template <typename E, int D, int QB>
 __device__ __forceinline__ void attend_rows(const AttentionArgs &a, const Rows &r, int head, int t0, int t1, int turn,
-                                            const Parts &parts, ChunkTiles<D> &lds, int lane, int wave) {
+                                            int64_t parts, ChunkTiles<D> &lds, int lane, int wave) {
   constexpr int KT = kChunkKeys, GROUPS = KT / 16;
   typedef GroupLoads<D> Loads;
   const Paged &b = a.b;
@@ -595,7 +592,7 @@ __device__ __forceinline__ void attend_rows(const AttentionArgs &a, const Rows &
     const int row = first_row + 32 * x + lane % 32;
     const float l = other_half_sum(w.l[x]);
     if (row >= end_row) continue;
-    const Place place = place_of(a, r, head, row, parts.of(row - r.first), w.m[x], l, lane < 32);
+    const Place place = place_of(a, r, head, row, part_of(parts, row - r.first), w.m[x], l, lane < 32);
 #pragma unroll
     for (int i = 0; i < D / 32; ++i)
 #pragma unroll
@@ -623,7 +620,7 @@ __global__ __launch_bounds__(256, kChunksPerCu<D>) void attention_chunk_kernel(c
   const int head = blockIdx.x % a.b.kv_heads, tile = a.tiles - 1 - blockIdx.x / a.b.kv_heads;
   const Rows r = rows_of<128 * QB>(a, tile, lane);
   if (r.count == 0) return;
-  attend_rows<E, D, QB>(a, r, head, r.lo / KT, (r.hi + KT - 1) / KT, 0, Parts{-1, 0}, lds, lane, wave);
+  attend_rows<E, D, QB>(a, r, head, r.lo / KT, (r.hi + KT - 1) / KT, 0, -1, lds, lane, wave);
 }
 
 // Where there are few row tiles: the key tiles of all row tiles and heads, one behind
@@ -720,7 +717,7 @@ __global__ __launch_bounds__(256, kChunksPerCu<D>) void attention_balanced_kerne
     const int begin = r.lo / KT, last = (r.hi + KT - 1) / KT, whole = (from + share - 1) / share * share;
     __syncthreads();  // the tiles of the last rows have been read
     attend_rows<E, D, QB>(a, r, head, begin + from, min(begin + to, last), whole < min(to, last - begin) ? whole - from : 0,
-                          from == 0 && to == size ? Parts{-1, 0} : Parts{((int64_t)2 * g + (from == 0)) * BM, 1}, lds, lane, wave);
+                          from == 0 && to == size ? -1 : ((int64_t)2 * g + (from == 0)) * BM, lds, lane, wave);
     end -= to - from;
   }
 }
@@ -786,8 +783,10 @@ __global__ __launch_bounds__(256) void attention_gather_kernel(const AttentionAr
 // Up to 32 rows: the waves share them and split the keys, each with a place of its
 // own for a tile's keys and one for its values, loaded again as soon as they have
 // been read, so that nothing waits for another wave before the end and a wave
-// always has loads in flight.  Keys and values are read once and marked so (64
-// sequences of up to 8192 keys: 163 us for 181).  Eight waves of 16 KiB: a wave's chain of products and
+// always has loads in flight.  Keys and values are marked as read once (64
+// sequences of up to 8192 keys: 163 us for 181), which they are where a sequence has one
+// row tile; where it has several (a chunk among single tokens, more than 32 query
+// heads to a key head) each of them asks for them.  Eight waves of 16 KiB: a wave's chain of products and
 // weights is long for a single query, and two to a SIMD hide it better than more
 // tiles ahead of fewer waves.
 template <int D>
@@ -812,7 +811,7 @@ __global__ __launch_bounds__(64 * Few<D>::W) void attention_few_kernel(const Att
 
   const int begin = r.lo / KT, all = max(0, (r.hi + KT - 1) / KT - begin), per = (all + a.splits - 1) / a.splits;
   const int t0 = begin + min(split * per, all), t1 = begin + min((split + 1) * per, all);
-  const Parts parts{a.splits > 1 ? (((int64_t)tile * b.kv_heads + head) * a.splits + split) * 32 : -1, 1};
+  const int64_t parts = a.splits > 1 ? (((int64_t)tile * b.kv_heads + head) * a.splits + split) * 32 : -1;
   Tile w;
   w.start(a, r, head, 0, lane);
 
@@ -907,7 +906,7 @@ __global__ __launch_bounds__(64 * Few<D>::W) void attention_few_kernel(const Att
       sum = fmaf(stats[1][v][row], __builtin_amdgcn_exp2f((m - big) * a.c), sum);
       o += *reinterpret_cast<const f32x4 *>(sums + (v * 32 + row) * D + sum_at(row, d / 4));
     }
-    place_of(a, r, head, r.first + row, parts.of(row), big, sum, d == 0).put<E>(d, o);
+    place_of(a, r, head, r.first + row, part_of(parts, row), big, sum, d == 0).put<E>(d, o);
   }
 }
 
