@@ -923,25 +923,31 @@ __global__ __launch_bounds__(256) void attention_join_kernel(const AttentionArgs
       m = a.stats[2 * (first + lane * 32)];
       l = a.stats[2 * (first + lane * 32) + 1];
     }
-    // eight splits' parts are in flight; those of splits without keys hold zeros
-    f32x4 o{0, 0, 0, 0};
     const float top = wave_reduce<MaxF>(m);
     const float f = m == -__builtin_inff() ? 0.0f : __builtin_amdgcn_exp2f((m - top) * a.c);
     const float sum = wave_reduce<SumF>(f * l);  // a split without keys has l = 0; one whose l is NaN counts whatever its m
     const float *part = a.part + first * a.b.dim + 4 * lane;
-    for (int base = 0; base < a.splits; base += 8) {
-      f32x4 v[8];
+    // eight splits' parts are in flight; those of splits without keys hold zeros
+    const auto joined = [&](auto scaled) {
+      f32x4 o{0, 0, 0, 0};
+      for (int base = 0; base < a.splits; base += 8) {
+        f32x4 v[8];
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        v[i] = f32x4{0, 0, 0, 0};
-        if (base + i < a.splits && 4 * lane < a.b.dim) v[i] = *reinterpret_cast<const f32x4 *>(part + (int64_t)(base + i) * 32 * a.b.dim);
-      }
+        for (int i = 0; i < 8; ++i) {
+          v[i] = f32x4{0, 0, 0, 0};
+          if (base + i < a.splits && 4 * lane < a.b.dim) v[i] = *reinterpret_cast<const f32x4 *>(part + (int64_t)(base + i) * 32 * a.b.dim);
+        }
 #pragma unroll
-      for (int i = 0; i < 8; ++i) {
-        const float fs = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), (base + i) % 64));
-        if (base + i < a.splits) o += rescaled(v[i], fs);
+        for (int i = 0; i < 8; ++i) {
+          const float fs = __builtin_bit_cast(float, __builtin_amdgcn_readlane(__builtin_bit_cast(int, f), (base + i) % 64));
+          if (base + i < a.splits) o += scaled(v[i], fs);
+        }
       }
-    }
+      return o;
+    };
+    f32x4 o = joined([](f32x4 v, float fs) { return v * fs; });
+    const f32x4 z = o * 0.0f;
+    if (__any(!(z[0] + z[1] + z[2] + z[3] == 0.0f))) o = joined(rescaled);  // rare, and 0.3 us for all rows
     const Place place = place_of(a, r, head, r.first + x, -1, top, sum, lane == 0);
     if (4 * lane < a.b.dim) place.put<E>(4 * lane, o);
   }
