@@ -21,12 +21,18 @@ constexpr int64_t kChunkRows = 128;
 
 // Whether equal shares of the key tiles are faster than a workgroup to a row tile
 // and head: `units` key tiles that every row tile has, `busy` of these, in the times
-// of a key tile measured with one workgroup to a CU and with all that it holds.
-// Counting the shares and joining their parts takes about kJoin.  With 128 dimensions
-// and 64 heads to 8: 517 new tokens over 31000 (264 row tiles and heads) 590 us by
-// shares, 822 without; 100 over 30000 93 and 590; 256 over 2000 49 and 50; 512 over
-// 4000 109 and 95.  Without cached tokens the first row tiles are short and a share
-// has many (2000 new tokens 122 and 58): only cached ones count.
+// of a key tile measured with one workgroup to a CU (alone) and with all that it holds
+// (full).  Between, some CUs hold one and some two, and the last of these ends the
+// launch: 1.7 us to a key tile of 128 dimensions at 264 workgroups, 1.9 at 448, 2.1 at
+// 504, for which 0.8 of the full time stands.  Counting the shares and joining their
+// parts takes about kJoin.  With 128 dimensions and 64 heads to 8, us by shares and
+// without (* the choice): 100 new tokens over 30000 93* and 590; 528 over 31000 611*
+// and 813, over 8000 179* and 208, over 2000 75 and 68*; 640 over 31000 709* and 809,
+// over 8000 214* and 221; 768 over 31000 838* and 855, over 8000 252 and 238*; 256 over
+// 2000 49* and 50; 512 over 4000 109 and 95*.  From 512 workgroups on there are no
+// shares, whatever the last round of workgroups leaves idle (1008 over 31000 1014, 1040,
+// of 520 workgroups, 1588).  Without cached tokens the first row tiles are short and a
+// share has many (2000 new tokens 122 and 58): only cached ones count.
 constexpr double kJoin = 25.0;  // us
 bool shares_pay(double units, int64_t busy, int64_t shares, int64_t dim) {
   const double alone = dim <= 64 ? 0.8 : dim <= 128 ? 1.4 : 2.6, full = dim <= 64 ? 1.4 : dim <= 128 ? 2.5 : 2.6;

@@ -97,7 +97,8 @@ class PagedAttention:
 
         seq_starts: int32 [seqs + 1] on the device, or None: a row to a sequence.  Rows of the result behind
         the last sequence are left as they were.  positions: int32 [rows], or None: the places in the cache.
-        max_kv_len: what no length passes, 0: whatever the page table holds.
+        max_kv_len: what no length passes, 0: whatever the page table holds, which divides the work of short
+        sequences as if they were as long.
         """
         import torch
 

@@ -45,6 +45,8 @@ class LogitRules:
 
     A history of up to max_history tokens to a row, kept here: `history` int32 [max_rows][max_history] and
     `total_len` int32 [max_rows], of which the first prompt_len (int32 [max_rows], None: 0) were given.
+    Once a history is full every further token takes the last place, and the one that stood there counts no
+    longer: max_history is the length that the text may reach, prompt and all.
     repetition, frequency, presence: fp32 [max_rows] or None; bias_index int32 and bias_value fp32
     [max_rows][n] or None; mask: int32 [max_rows][ceil(vocab / 32)] or None, a bit to a token, 0: forbidden.
     All of it lies on `device` and is read when the work runs, so the caller may change the values between two

@@ -563,7 +563,8 @@ typedef struct {
   int64_t tokens, seqs;          /* rows of q; sequences.  At most 2^24, and tokens * heads at most 2^30 (what one
                                     launch cannot do is refused before that) */
   int64_t max_kv_len;            /* what no kv_lens[s] passes (0: table_pages * page_size).  It decides how the
-                                    work is divided, not what is computed */
+                                    work is divided, not what is computed: a bound far above the lengths (that
+                                    of a long table) can take twice the time */
   const int32_t *seq_starts, *kv_lens, *page_table;
   int64_t table_ld, table_pages; /* table_ld at least table_pages; table_pages * page_size at most 2^31 - 2^16 */
   void *k_cache, *v_cache;       /* 16-byte aligned */
