@@ -51,6 +51,8 @@ class PagedAttention:
         dtype = torch.float16 if dtype is None else dtype
         if dtype not in (torch.float16, torch.bfloat16):
             raise ValueError(f"dtype: {dtype}, not fp16 or bf16")
+        if not 0 <= window < 1 << 31:  # attention alone takes it, behind an append that would have run
+            raise ValueError(f"window: {window}, not in [0, 2^31)")
         self.F, self.heads, self.kv_heads, self.dim, self.window, self.eps = F, heads, kv_heads, dim, window, eps
         self.dtype, self.scale, self.pairs, self.rope_scale = dtype, 1 / math.sqrt(dim), pairs, rope_scale
         self.rotary_dim = dim if rotary_dim is None else rotary_dim

@@ -1,10 +1,10 @@
-"""The longest sequence that a page table may describe: the kernels' 32-bit places reach beyond its last key (no GPU needed)."""
+"""The longest sequence that a page table may describe, whose 32-bit places the kernels go beyond, and the widest window (no GPU needed)."""
 import ctypes
 
 import pytest
 
 from tests import attention_launches as L
-from tests.test_attention_host import append_args, attention_args, fb  # noqa: F401
+from tests.test_attention_host import append_args, attention_args, calls, fb, layer  # noqa: F401
 
 MOST = 2 ** 31 - 2 ** 16
 AHEAD = 8 * 32 + 31 * 8 * 32 + 64  # keys that a look-up, a load or a count of tiles goes beyond the last one: see below
@@ -24,3 +24,12 @@ def test_longer_tables_are_refused(fb, page):  # noqa: F811
         if status:
             assert fb.raw_status("fluxbin_paged_attention", *attention_args(fb, batch=b)) == status
             assert fb.raw_status("fluxbin_rope_append", *append_args(fb, batch=b)) == status
+
+
+@pytest.mark.parametrize("window", [-1, 1 << 31, 1 << 32])
+def test_windows_that_attention_would_refuse_or_misread(calls, window):  # noqa: F811
+    """Refused before anything is appended: 2^32 would have come through as 0, no window."""
+    with pytest.raises(ValueError, match="window"):
+        layer(window=window)
+    assert not calls
+    assert layer(window=(1 << 31) - 1).window == 2 ** 31 - 1
