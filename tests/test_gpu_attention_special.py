@@ -99,18 +99,19 @@ def test_scores_at_the_ends_of_fp32(fb, form, dt, sign):
     same_as(*attend(fb, c, 1e30), out, lse, tol, tol_lse)
 
 
+@pytest.mark.parametrize("dim", [64, 72, 128, 256])
 @pytest.mark.parametrize("dt", ["f16", "bf16"])
 @pytest.mark.parametrize("form", FORMS)
-def test_infinite_values_under_vanishing_weights(fb, form, dt):
+def test_infinite_values_under_vanishing_weights(fb, form, dt, dim):
     """A weight is positive however small: an infinity shows, whether it comes before the maximum or after it."""
-    note(f"infinities under weights of e^-300, {form} {dt}")
-    c = make(form, dt)
+    note(f"infinities under weights of e^-300, {form} {dt} dim {dim}")
+    c = make(form, dt, dim)
     workspace_of(fb, c)
     c.q.fill_(1)
     c.k.mul_(0.01)
     n = c.lens_host[0] - c.lengths[0][0]
     for p, i in keys(c, 0, list(range(64)) + list(range(n - 20, n - 8))):
-        c.k[p, :, i] = -300 / 128
+        c.k[p, :, i] = -300 / dim
     _, _, mag, work, seen = attention_oracle(c, 1.0)
     for j, d, v in ((5, 3, math.inf), (n - 10, 4, -math.inf), (7, 5, math.inf), (n - 12, 5, -math.inf), (9, 6, math.nan), (n - 13, 7, math.nan)):
         p, i = keys(c, 0, [j])[0]
@@ -168,3 +169,17 @@ def test_outputs_over_the_queries(fb, form, dt):
         torch.cuda.synchronize()
         assert torch.isinf(apart).any() == bad
         assert torch.equal(q, apart)
+
+
+@pytest.mark.parametrize("dim", [64, 72, 256])
+@pytest.mark.parametrize("form", FORMS)
+def test_a_query_that_is_not_a_number(fb, form, dim):
+    note(f"NaN query, {form} dim {dim}")
+    c = make(form, "bf16", dim, seed=4)
+    assert (workspace_of(fb, c) > 0) == (form in ("splits", "shares"))
+    _, _, mag, work, seen = attention_oracle(c, 0.05)
+    c.q[-1, dim - 1] = math.nan
+    out, lse, *_ = attention_oracle(c, 0.05)
+    assert np.isnan(lse).sum() == 1 and np.isnan(out[-1, 0]).all()
+    tol, tol_lse = attention_bounds(c, np.nan_to_num(out), mag, work, seen)
+    same_as(*attend(fb, c, 0.05), out, lse, tol, tol_lse)
